@@ -262,6 +262,35 @@ OSC_API int osc_linear_fp8_fallback(const uint8_t* QX8, const uint8_t* SX, const
                             const uint8_t* SW, int M, int N, int K, uint16_t* Y, float* Yf32,
                             osc_stream_t stream);
 
+/* The producer step of a module on the §4 fallback, with the residual stream in front of it:
+ * residual addition, RMSNorm and MXFP8 quantization of each row in one pass. Per row
+ *     h = X + res,  y = h * gamma / sqrt(mean(h^2) + eps),
+ * QX8 (M x K E4M3 codes) and SX (osc_scale_bytes(M, K, 0)) the quantization of y as in
+ * osc_quantize_fp8 (their product with a weight: osc_linear_fp8_fallback), H = bf16(h) the new
+ * residual stream and Y = bf16(y) the normed rows (for a router, or for osc_gemv). Sums and
+ * products are fp32; h enters the norm unrounded and y enters QX8 and Y unrounded, so each output
+ * is rounded once (unlike osc_rmsnorm_quantize, which quantizes bf16 rows). res (M x K bf16) may
+ * be NULL (h = X); H and Y (M x K bf16) may each be NULL (not written). H may be X or res itself
+ * (the stream updated in place); otherwise no output may overlap an input or another output.
+ * eps >= 0; an all-zero row with eps = 0 gives zeros. fp32 sums: |h| below 1e18. K at most 32768. */
+OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res, const uint16_t* gamma, float eps,
+                                         int M, int K, uint16_t* H, uint16_t* Y, uint8_t* QX8, uint8_t* SX,
+                                         osc_stream_t stream);
+
+/* The layer for a few token rows with the activations left in bf16 (decoding, where the weight
+ * stream bounds the step and 4-bit activations save nothing), on the weights of
+ * osc_prepare_weight:
+ *     Y[m][n] = sum_{k not in the table} X[m][k] qW[n][k] 2^eW  +  sum_i X[m][ch_i] W_L[n][i]
+ * with ch_i the channel of table entry i: the table's channels meet their bf16 weights W_L, as in
+ * the §3.2 equation, and no other value is quantized. X: M x K bf16. L, R, K_L, WL as
+ * osc_quantize and osc_linear; L = NULL with K_L = 0 multiplies by the 4-bit weights alone. Y: M x N
+ * bf16, rounded once from fp32 sums; Yf32 (M x N fp32) may be NULL. One launch, no workspace, any
+ * order of calls gives the same bits. For any M up to 1048560, but the weights are read again for
+ * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights
+ * must be below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). A bad table (an entry >= G, more entries than K_L) is recorded in the status word. */
+OSC_API int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
+                     const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);
+
 /* ---- grouped (MoE) form, §1 and §5.2 (Qwen3-30B-A3B expert layers) -------------------
  * Tokens arrive sorted by expert: expert e owns rows off[e] .. off[e+1] of X. The grouped
  * calls work on a PADDED row space in which expert e's rows start at poff[e], a multiple of
@@ -293,6 +322,20 @@ OSC_API int osc_linear_grouped(const uint8_t* QX, const uint8_t* SX, const uint1
                        const uint8_t* QW, const uint8_t* SW, const uint16_t* WL,
                        const int* mblock_expert, const int* kl, int E, int Mp, int N, int K,
                        int G, int K_L, uint16_t* Y, float* Yf32, osc_stream_t stream);
+
+/* osc_gemv for routed rows: row r of Y is X row r / fan times the weight of expert[r], with that
+ * expert's table and W_L. fan is the number of consecutive rows that share an X row: the router's
+ * top-k for the gate and up projection (X one row per token, expert the tokens' choices in
+ * order), 1 for the down projection (X one row per choice). expert: `rows` ids on the DEVICE, in
+ * any order and with any repetition, read by the kernel, so a decoding step needs no plan on the
+ * host and no sorting; each chosen expert's weight is read once for every 8 or 16 of its rows. An
+ * id < 0 marks an unused row: its Y is zeros. An id >= E is recorded in the status word
+ * (OSC_ERR_TABLE) and its row is zeros too. X: (rows + fan - 1) / fan x K; L, QW, SW, WL per expert
+ * as in osc_quantize_grouped and osc_linear_grouped (L may be NULL when K_L == 0). Y: rows x N bf16;
+ * Yf32 (rows x N) may be NULL. rows and E at most 4096 each: for more rows use osc_linear_grouped. */
+OSC_API int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, int E, int K, int G,
+                             const int8_t* L, int R, int K_L, const uint8_t* QW, const uint8_t* SW,
+                             const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);
 
 /* Reads and clears the current device's status word in one atomic exchange on `stream`, then
  * synchronizes `stream`. Returns OSC_OK, OSC_ERR_TIMEOUT or OSC_ERR_TABLE; *raw (may be NULL)

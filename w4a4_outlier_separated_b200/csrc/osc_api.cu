@@ -284,6 +284,20 @@ int check_linear_common(const void* QX, const void* SX, const void* QW, const vo
   return OSC_OK;
 }
 
+// Arguments that the two 4-bit matrix-vector products share.
+int check_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
+               const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32) {
+  if (R < 1 || R > osc::MAX_R) return OSC_ERR_ARG;
+  if (!X || !QW || !SW || !Y || M < 0 || N <= 0 || K <= 0 || K_L < 0) return OSC_ERR_ARG;
+  if ((long long)(N + 127LL) * (K / 32) >= (1LL << 31)) return OSC_ERR_ARG;
+  if (L == nullptr && K_L != 0) return OSC_ERR_ARG;
+  if (K_L > 0 && !WL) return OSC_ERR_ARG;
+  if (K_L > 32767 || (L != nullptr && (long long)(K / G) * R > osc::MAX_TAB)) return OSC_ERR_ARG;
+  if (!a16(X) || !a16(QW) || !a16(SW) || !a16(Y) || (WL && !a16(WL)) || (Yf32 && !a16(Yf32))) return OSC_ERR_ALIGN;
+  if (K % 256 != 0 || N % 16 != 0 || K_L % 16 != 0) return OSC_ERR_ALIGN;
+  return OSC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -667,6 +681,52 @@ int osc_linear_grouped(const uint8_t* QX, const uint8_t* SX, const uint16_t* B, 
   const int kind = G == 16 ? osc::KIND_MXF4_B16 : osc::KIND_MXF4_B32;
   return run_gemm(kind, QX, SX, B, QW, SW, WL, Mp, N, K, K_L, E, mblock_expert, K_L > 0 ? kl : nullptr, Y, Yf32,
                   (cudaStream_t)stream);
+}
+
+int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res, const uint16_t* gamma, float eps, int M,
+                                 int K, uint16_t* H, uint16_t* Y, uint8_t* QX8, uint8_t* SX, osc_stream_t stream) {
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return OSC_ERR_ARG;
+  if (M == 0 && K > 0) return OSC_OK;                       // nothing to read or write
+  if (!X || !gamma || !QX8 || !SX || M < 0 || K <= 0) return OSC_ERR_ARG;
+  if (K > osc::AN_MAX_K) return OSC_ERR_ARG;
+  if ((long long)(M + 127LL) * (K / 32) >= (1LL << 31)) return OSC_ERR_ARG;
+  if (!a16(X) || !a16(gamma) || !a16(QX8) || !a16(SX) || (res && !a16(res)) || (H && !a16(H)) || (Y && !a16(Y)))
+    return OSC_ERR_ALIGN;
+  if (K % 256 != 0) return OSC_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  int rc = device_state(&ds);
+  if (rc != OSC_OK) return rc;
+  osc::AddNormParams p{X, res, gamma, eps, M, K, H, Y, QX8, SX, 1};
+  return launch_result(osc::launch_add_rmsnorm_fp8(p, ds->sms, (cudaStream_t)stream));
+}
+
+int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
+             const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream) {
+  if (!valid_g(G)) return OSC_ERR_G;
+  if (M == 0 && N > 0 && K > 0 && K_L >= 0) return OSC_OK;  // nothing to read or write
+  int rc = check_gemv(X, M, K, G, L, R, K_L, QW, SW, WL, N, Y, Yf32);
+  if (rc != OSC_OK) return rc;
+  if (M > 65535 * 16) return OSC_ERR_ARG;
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != OSC_OK) return rc;
+  osc::GemvParams p{X, M, N, K, G, L, R, K_L, QW, SW, WL, Y, Yf32, ds->status, nullptr, 1, 1};
+  return launch_result(osc::launch_gemv(p, ds->sms, (cudaStream_t)stream));
+}
+
+int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, int E, int K, int G, const int8_t* L,
+                     int R, int K_L, const uint8_t* QW, const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y,
+                     float* Yf32, osc_stream_t stream) {
+  if (!valid_g(G)) return OSC_ERR_G;
+  if (E <= 0 || E > osc::GEMV_MAX_EXPERTS || fan < 1) return OSC_ERR_ARG;
+  if (rows == 0 && N > 0 && K > 0 && K_L >= 0) return OSC_OK;  // nothing to read or write
+  int rc = check_gemv(X, rows, K, G, L, R, K_L, QW, SW, WL, N, Y, Yf32);
+  if (rc != OSC_OK) return rc;
+  if (!expert || rows > osc::GEMV_MAX_ROWS) return OSC_ERR_ARG;
+  if (!a16(expert)) return OSC_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  if ((rc = device_state(&ds)) != OSC_OK) return rc;
+  osc::GemvParams p{X, rows, N, K, G, L, R, K_L, QW, SW, WL, Y, Yf32, ds->status, expert, fan, E};
+  return launch_result(osc::launch_gemv(p, ds->sms, (cudaStream_t)stream));
 }
 
 int osc_selftest_timeout(int limit_us, osc_stream_t stream) {

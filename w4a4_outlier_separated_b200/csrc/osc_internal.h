@@ -70,6 +70,45 @@ constexpr int NQ_MAX_K = 6144;
 // tmX: X as (32-channel blocks) x 64 bytes, box {32, K/32} (one row per box), 64-byte swizzle
 cudaError_t launch_rmsnorm_quantize(const CUtensorMap& tmX, const NormQuantParams& p, int num_sms, cudaStream_t s);
 
+// Residual addition + RMSNorm + MXFP8 quantization (osc_norm.cu).
+struct AddNormParams {
+  const uint16_t* X;       // M x K bf16
+  const uint16_t* res;     // M x K bf16 or nullptr
+  const uint16_t* gamma;   // K bf16
+  float eps;
+  int M, K;
+  uint16_t* H;             // M x K bf16, the sum, or nullptr (may be X or res itself)
+  uint16_t* Y;             // M x K bf16, the normed rows, or nullptr
+  uint8_t* Q;              // M x K E4M3 codes
+  uint8_t* S;              // scales in the MMA layout
+  int rows_per_cta;        // set by the launcher
+};
+// largest K: 1024 threads of a row with 4 steps of 8 channels each
+constexpr int AN_MAX_K = 32768;
+cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s);
+
+// Few bf16 token rows times a prepared 4-bit weight (osc_gemv.cu); grouped when `expert` is set.
+struct GemvParams {
+  const uint16_t* X;       // rows of K bf16
+  int M, N, K, G;
+  const int8_t* L;         // K/G x R entries (per expert) or nullptr
+  int R, K_L;
+  const uint8_t* QW;       // N x K/2 (per expert)
+  const uint8_t* SW;       // scales in the MMA layout (per expert)
+  const uint16_t* WL;      // N x K_L (per expert)
+  uint16_t* Y;             // M x N
+  float* Yf32;             // M x N or nullptr
+  int* status;
+  const int* expert;       // grouped: M expert ids (device); nullptr = dense
+  int fan, E;              // grouped: row r reads X row r / fan
+  // set by the launcher
+  int S, n_units, mt, stages;
+};
+// grouped form: most rows and experts of one call (their ids are staged in shared memory)
+constexpr int GEMV_MAX_ROWS = 4096;
+constexpr int GEMV_MAX_EXPERTS = 4096;
+cudaError_t launch_gemv(const GemvParams& p, int num_sms, cudaStream_t s);
+
 struct GroupedQuantParams {
   const uint16_t* X;          // off[E] x K bf16, expert-sorted
   const int* off;             // E+1 (device)

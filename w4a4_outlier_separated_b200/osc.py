@@ -66,6 +66,9 @@ def lib() -> ctypes.CDLL:
             "osc_grouped_plan": ([P, i32, P, P, P, i32], i32),
             "osc_quantize_grouped": ([P, i32, i32, P, P, P, i32, i32, i32, P, i32, i32, P, P, P, P], i32),
             "osc_linear_grouped": ([P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P, P], i32),
+            "osc_add_rmsnorm_quantize_fp8": ([P, P, P, f32, i32, i32, P, P, P, P, P], i32),
+            "osc_gemv": ([P, i32, i32, i32, P, i32, i32, P, P, P, i32, P, P, P], i32),
+            "osc_gemv_grouped": ([P, i32, i32, P, i32, i32, i32, P, i32, i32, P, P, P, i32, P, P, P], i32),
             "osc_status": ([P, P], i32),
             "osc_selftest_timeout": ([i32, P], i32),
             "osc_set_tile_n": ([i32], i32),
@@ -299,6 +302,86 @@ def osc_linear_grouped(QX, SX, B, QW, SW, WL, mblock_expert, kl, E: int, Mp: int
                                                           _ptr(SW), _ptr(WL) if K_L else None, _ptr(mblock_expert),
                                                           _ptr(kl), E, Mp, N, K, G, K_L, _ptr(Y), _ptr(Yf32),
                                                           _stream(stream)))
+
+
+def _rows(name: str, t, n: int, device, itemsizes):
+    """Address of a dense CUDA tensor of n elements of an allowed size on `device` (None: None)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.numel() != n or t.element_size() not in itemsizes:
+        raise ValueError(f"{name}: expected {n} elements of {itemsizes} bytes, got {t.numel()} of {t.element_size()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _call_on(device, name: str, args, stream):
+    """Call lib().name(*args, stream) with `device` current (its current stream unless one is given)."""
+    if device.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"expected a stream of {device}, got one of {stream.device}")
+    index = device.index
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+    if rc != OSC_OK:
+        _check(name, rc)
+
+
+def osc_add_rmsnorm_quantize_fp8(X, res, gamma, eps: float, H, Y, QX8, SX, stream=None):
+    """h = X + res (res None: X), y = RMSNorm(h) * gamma: MXFP8 codes and scales of y into QX8 and SX,
+    bf16(h) into H and bf16(y) into Y where they are given. H may be X or res."""
+    M, K = X.shape
+    d = X.device
+    n = M * K
+    _call_on(d, "osc_add_rmsnorm_quantize_fp8",
+             (_rows("X", X, n, d, (2,)), _rows("res", res, n, d, (2,)), _rows("gamma", gamma, K, d, (2,)), eps, M, K,
+              _rows("H", H, n, d, (2,)), _rows("Y", Y, n, d, (2,)), _rows("QX8", QX8, n, d, (1,)),
+              _rows("SX", SX, (M + 127) // 128 * 4 * K, d, (1,))), stream)
+
+
+def _gemv_operands(E: int, K: int, G: int, L, K_L: int, QW, SW, WL, N: int, d):
+    """(address of L, slots per group, addresses of QW, SW and WL) of E experts' prepared weights."""
+    V = 16 if G == 16 else 32
+    R = 1 if L is None else _slots(L, E * max(1, K // G))
+    return (_rows("L", L, E * (K // G) * R, d, (1,)), R, _rows("QW", QW, E * N * (K // 2), d, (1,)),
+            _rows("SW", SW, E * ((N + 127) // 128) * 128 * (K // V), d, (1,)),
+            _rows("WL", WL, E * N * K_L, d, (2,)) if K_L else None)
+
+
+def osc_gemv(X, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
+    """Y (M x N) = X (M x K bf16, not quantized) times prepared 4-bit weights, the table's channels
+    taken from W_L; for a few rows (decoding)."""
+    if G not in (16, 32, 64):
+        _check("osc_gemv", -3)
+    M, K = X.shape
+    d = X.device
+    l, R, qw, sw, wl = _gemv_operands(1, K, G, L, K_L, QW, SW, WL, N, d)
+    _call_on(d, "osc_gemv", (_rows("X", X, M * K, d, (2,)), M, K, G, l, R, K_L, qw, sw, wl, N,
+                             _rows("Y", Y, M * N, d, (2,)), _rows("Yf32", Yf32, M * N, d, (4,))), stream)
+
+
+def osc_gemv_grouped(X, fan: int, expert, E: int, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
+    """Row r of Y (rows x N) = X row r // fan times the prepared weight of expert[r] (int32 CUDA
+    tensor of `rows` ids, < 0: a row of zeros)."""
+    if G not in (16, 32, 64):
+        _check("osc_gemv_grouped", -3)
+    if expert.dtype != torch.int32:
+        raise ValueError("expert: expected an int32 tensor")
+    Mx, K = X.shape
+    rows, d = expert.numel(), X.device
+    if fan < 1 or Mx != (rows + fan - 1) // fan:
+        raise ValueError(f"{rows} rows with fan {fan} need {-(-rows // max(1, fan))} rows of X, got {Mx}")
+    l, R, qw, sw, wl = _gemv_operands(E, K, G, L, K_L, QW, SW, WL, N, d)
+    _call_on(d, "osc_gemv_grouped", (_rows("X", X, Mx * K, d, (2,)), rows, fan, _rows("expert", expert, rows, d, (4,)), E, K,
+                                     G, l, R, K_L, qw, sw, wl, N, _rows("Y", Y, rows * N, d, (2,)),
+                                     _rows("Yf32", Yf32, rows * N, d, (4,))), stream)
 
 
 def osc_selftest_timeout(limit_us: int = 10000, stream=None):
