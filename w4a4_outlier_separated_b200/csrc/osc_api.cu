@@ -117,6 +117,13 @@ int launch_result(cudaError_t e) { return e == cudaSuccess ? OSC_OK : fail_cuda(
 
 }  // namespace
 
+namespace osc {
+cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
+  return make_map(m, dt, rank, base, dims, strides, box, sw) == OSC_OK ? cudaSuccess : (cudaError_t)t_last_cuda;
+}
+}  // namespace osc
+
 namespace {
 
 // The split plan of the few-row product: S parts of K per 128-row weight tile, so that

@@ -5,10 +5,12 @@
 //
 // Unit: 32 weight rows, the four octets {q*32 + j*8 .. +7} (q = 0..3) of a 128-row block, because
 // the scale layout keeps exactly those rows' words together: 128 contiguous bytes per 512-byte
-// atom. A CTA (or a cluster of S CTAs that split K) owns a unit. Its warps take chunks of 128
-// channels in turn; a warp copies a chunk's codes, scales and token rows into its own stages of
-// shared memory with cp.async and computes without waiting for any other warp. The warps' sums
-// meet once, in shared memory (across the cluster in distributed shared memory), in a fixed order.
+// atom. Item: a unit's codes and scales of 128 channels, or its W_L of 32 columns (both 64 bytes a
+// row). A CTA stages the tokens once, then runs over its units; a team of its warps shares a unit's
+// items. Each warp copies its items into its own ring of stages with cp.async, running ahead over
+// the ends of units, and computes without waiting for another warp. A unit's sums meet in the
+// stages just consumed, in a fixed order. Where one CTA cannot hold the tokens, or the units are
+// fewer than the SMs, a cluster of S CTAs splits K and adds its sums through distributed shared memory.
 //
 // Arithmetic: mma.m16n8k16 on f16 operands with fp32 accumulators, the weight rows as the
 // 16-row side and the tokens as the 8-wide side. E2M1 codes become f16 exactly (one conversion
@@ -17,9 +19,10 @@
 // 2^-31 of that maximum, and below that errs by at most 2^-39 of it, far under the fp32 sum's own
 // rounding. A scale block's products are summed in fp32, then multiplied by the weight's and the
 // token's powers of two (exact) and added in fp32. Y is rounded once.
-// The protected channels are zeroed in the staged tokens; their products run as bf16 mma of the
-// gathered tokens with W_L into the same sums.
+// The protected channels are zeroed in the staged tokens and kept apart in bf16; their products
+// with W_L run as bf16 mma into the same sums.
 #include <cuda_fp16.h>
+#include <cstdlib>
 
 #include "osc_device.cuh"
 #include "osc_internal.h"
@@ -28,50 +31,14 @@ namespace osc {
 
 namespace {
 
-constexpr int GV_WARPS = 8;
 constexpr int GV_ROWS = 32;                       // weight rows of a unit
-constexpr int GV_CHUNK = 128;                     // channels of a chunk
-constexpr int GV_WBYTES = GV_ROWS * GV_CHUNK / 2; // codes of a stage
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
-  const int n = full ? 16 : 0;                    // 0: the 16 bytes are filled with zeros, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
-  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" :: "r"(a), "r"(v.x), "r"(v.y) : "memory");
-}
-__device__ __forceinline__ void sts32f(uint32_t a, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" :: "r"(a), "f"(v) : "memory");
-}
-__device__ __forceinline__ float lds32f(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ float lds32f_cluster(uint32_t a) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
@@ -94,14 +61,31 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same onto zero
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^(byte - 127) (0 stands for 2^-127, a subnormal).
-__device__ __forceinline__ float e8m0(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+// The four scales 2^(byte - 127) of a layout word, through bf16 (exact, 2^-127 as its subnormal).
+__device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+  f[0] = __uint_as_float(lo << 16);
+  f[1] = __uint_as_float(lo & 0xFFFF0000u);
+  f[2] = __uint_as_float(hi << 16);
+  f[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -109,58 +93,105 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t redux_max(uint32_t v) {
+__device__ __forceinline__ int cluster_id() {
   uint32_t r;
-  asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
-  return r;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return (int)r;
 }
 
-// Shared memory of a CTA, in bytes from its start.
+// Shared memory of a CTA, in bytes from its start. CH: channels of an item; kc: channels of this
+// CTA's K range (at most); cols: W_L columns.
 struct GvSmem {
-  int stage, warp, chan, ids, flag, total;
+  int stage, warp, sc, x, red, xs, b, bcols, ent, ids, flag, at, total;
 };
-__host__ __device__ inline GvSmem gv_smem(int V, int mt, int stages, int n_list, int rows, int E) {
+// A warp's sums, [token][row]: the row pitch of 36 floats keeps the mma fragments' stores (tokens 2t,
+// rows g) and the reads (32 rows) off each other's banks.
+constexpr int GV_PITCH = 36;
+__host__ __device__ constexpr int gv_sums(int NT) { return 8 * NT * GV_PITCH * 4; }
+__host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST, int mt, int kc, int cols, int n_table,
+                                          int rows, int E) {
   GvSmem m;
-  m.stage = GV_WBYTES + GV_ROWS * 4 * (32 / V) + mt * 256 + 64;   // codes, scales, tokens, token scales
-  m.warp = stages * m.stage;
-  m.chan = GV_WARPS * m.warp;                                      // channel of each W_L column
-  m.ids = m.chan + (n_list + 31) / 32 * 32 * 4;                    // grouped: expert ids
+  m.stage = GV_ROWS * CH / 2;                                      // codes, or W_L columns
+  m.warp = ST * m.stage;
+  m.sc = NW * m.warp;                                              // the stages' scales
+  m.x = m.sc + NW * ST * GV_ROWS * CH / V;                         // tokens in f16
+  m.red = m.x + mt * kc * 2;                                       // two sets of the warps' sums (NT = 1)
+  m.xs = m.red + (NT == 1 ? 2 * NW * gv_sums(NT) : 0);             // the tokens' powers of two, per item
+  m.b = (m.xs + kc / CH * NT * 32 + 127) / 128 * 128;              // protected channels' values
+  m.bcols = ((cols < n_table ? cols : n_table) + 63) / 64 * 64;
+  m.ent = m.b + mt * m.bcols * 2;                                  // table entries with their columns
+  m.ids = m.ent + (n_table + 3) / 4 * 16;                          // grouped: expert ids
   m.flag = m.ids + (rows + 3) / 4 * 16;                            // grouped: experts with rows
-  m.total = m.flag + (E + 3) / 4 * 16;
+  m.at = m.flag + (E + 3) / 4 * 16;                                // stage that holds a warp's sums (NT = 2)
+  m.total = m.at + NW * 4 + 1024;                                  // and room to start at a multiple of 1024
   return m;
+}
+
+__device__ __forceinline__ void team_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace
 
-// V: channels of a scale slot; NT: token tiles of 8; ST: stages per warp.
-template <int V, int NT, int ST, bool GROUPED>
-__global__ void __launch_bounds__(GV_WARPS * 32, 2) gemv_kernel(GemvParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_scan[2][GV_WARPS];
-  __shared__ int s_list[16];
+// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp.
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+__global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  __shared__ uint64_t s_full[NW][ST];   // a stage's data has arrived
+  __shared__ int s_abort;
+  __shared__ int s_scan[2][NW];
+  __shared__ int s_cols[2];   // first W_L column of this CTA's K range, one past the last
+  __shared__ int s_list[16];  // this pass's rows of Y (grouped)
   __shared__ int s_slot[3];   // rows of this pass, where the next one starts, the expert
-  __shared__ float s_sum[GV_ROWS * 16];
+  __shared__ float s_sum[GV_ROWS * 8 * NT];
+  constexpr int THREADS = NW * 32;
+  constexpr int SLOT = 32 / V;                             // scale slots of a 32-channel block
+  constexpr int RB = CH / 2;                               // bytes of an item's row: codes, or CH / 4 W_L columns
+  constexpr int COLS = CH / 4;
+  constexpr int SBYTES = GV_ROWS * CH / V;                 // scales of an item
+  static_assert(NT == 1 || gv_sums(NT) <= GV_ROWS * RB, "a stage takes a warp's sums");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S;
-  const int unit = blockIdx.x / S, rank = blockIdx.x - unit * S;
-  const int N = p.N, K = p.K, nslot4 = K / V / 4;
-  const int n_table = p.L ? K / p.G * p.R : 0;
-  const GvSmem sm = gv_smem(V, p.mt, p.stages, min(n_table, p.K_L), GROUPED ? p.M : 0, GROUPED ? p.E : 0);
+  const int cta = S == 1 ? blockIdx.x : cluster_id(), rank = S == 1 ? 0 : cluster_ctarank(), n_cta = p.n_cta;
+  const int N = p.N, K = p.K;
+  const int n_table = p.L ? (K >> p.g_shift) * p.R : 0;
+  const GvSmem sm = gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t swarp = sbase + warp * sm.warp;
-  const int row0 = (unit >> 2) * 128 + (unit & 3) * 8;   // first row of octet 0; octet q is 32 q further
+  const int swarp = warp * sm.warp, sscale = sm.sc + warp * (ST * SBYTES);
+  const int tw = 1 << p.tw_shift, team = warp >> p.tw_shift, twarp = warp & (tw - 1);
+  auto ld32 = [&](int off) { return *reinterpret_cast<const uint32_t*>(smem + off); };
+  auto ld16 = [&](int off) { return (uint32_t)*reinterpret_cast<const uint16_t*>(smem + off); };
+  auto ld64 = [&](int off) { return *reinterpret_cast<const uint2*>(smem + off); };
+  auto ld128 = [&](int off) { return *reinterpret_cast<const uint4*>(smem + off); };
+  // this CTA's part of K, in items
+  const int c0 = rank * p.nc_base + min(rank, p.nc_more), nc = p.nc_base + (rank < p.nc_more ? 1 : 0);
+
+  // a warp's stages and their barriers are its own
+  const uint32_t bars = smem_u32(&s_full[warp][0]);
+  if (lane == 0) {
+    s_abort = 0;
+    for (int i = 0; i < ST; ++i) mbar_init(bars + i * 8, 1);
+    fence_barrier_init();
+    if (warp == 0) {
+      tma_prefetch_desc(&maps.w);
+      tma_prefetch_desc(&maps.s);
+      if (n_table) tma_prefetch_desc(&maps.wl);
+    }
+  }
+  __syncwarp();
 
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- which expert and which rows (grouped), which tokens (dense)
-  int e = 0, n_rows = p.M;
+  // ---- which expert (grouped)
+  int e = 0;
   int* const ids = reinterpret_cast<int*>(smem + sm.ids);
   if constexpr (GROUPED) {
     int* const flag = reinterpret_cast<int*>(smem + sm.flag);
-    for (int i = tid; i < p.E; i += GV_WARPS * 32) flag[i] = 0;
+    for (int i = tid; i < p.E; i += THREADS) flag[i] = 0;
     __syncthreads();
-    for (int r = tid; r < p.M; r += GV_WARPS * 32) {
+    for (int r = tid; r < p.M; r += THREADS) {
       const int id = p.expert[r];
       ids[r] = id;
       if (id >= 0 && id < p.E) flag[id] = 1;
@@ -169,10 +200,9 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 2) gemv_kernel(GemvParams p) {
     __syncthreads();
     if (blockIdx.y == 0) {
       // rows without an expert come out as zeros
-      for (int r = warp * S + rank; r < p.M; r += GV_WARPS * S) {
+      for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
         if (ids[r] >= 0 && ids[r] < p.E) continue;
-        const int n = row0 + (lane >> 3) * 32 + (lane & 7);
-        if (n < N) {
+        for (int n = tid; n < N; n += THREADS) {
           p.Y[(size_t)r * N + n] = 0;
           if (p.Yf32) p.Yf32[(size_t)r * N + n] = 0.f;
         }
@@ -196,48 +226,12 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 2) gemv_kernel(GemvParams p) {
     e = s_slot[2];
     if (e < 0) return;                                   // the same for the whole cluster
   }
-  const uint8_t* const QW = p.QW + (size_t)e * N * (K / 2);
-  const uint8_t* const SW = p.SW + (size_t)e * ((N + 127) / 128) * nslot4 * 512;
-  const uint16_t* const WL = p.WL + (size_t)e * N * p.K_L;
   const int8_t* const L = p.L + (size_t)e * n_table;
-
-  // ---- the channel of each W_L column (-1: a pad column, or a channel already taken)
-  int n_col = 0;
-  int* const chan = reinterpret_cast<int*>(smem + sm.chan);
-  if (n_table) {
-    int it = 0;
-    for (int b = 0; b < n_table; b += GV_WARPS * 32, it ^= 1) {
-      const int i = b + tid;
-      int v = i < n_table ? (int)L[i] : -1;
-      if (v >= p.G) {
-        if (unit == 0 && rank == 0) record_status(p.status, DEV_BAD_TABLE);
-        v = -1;
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, v >= 0);
-      if (lane == 0) s_scan[it][warp] = __popc(m);
-      __syncthreads();
-      int col = n_col + __popc(m & ((1u << lane) - 1u));
-      for (int w = 0; w < GV_WARPS; ++w) {
-        if (w < warp) col += s_scan[it][w];
-        n_col += s_scan[it][w];
-      }
-      if (v >= 0) {
-        if (col >= p.K_L) {
-          if (unit == 0 && rank == 0) record_status(p.status, DEV_BAD_TABLE);
-        } else {
-          bool again = false;
-          for (int r = 1; r <= i % p.R; ++r) again |= (int)L[i - r] == v;
-          chan[col] = again ? -1 : (i / p.R) * p.G + v;
-        }
-      }
-    }
-    n_col = min(n_col, p.K_L);
-    for (int i = n_col + tid; i < (n_col + 31) / 32 * 32; i += GV_WARPS * 32) chan[i] = -1;
-    __syncthreads();
-  }
-
-  const int c_end = (int)((long long)(K / GV_CHUNK) * (rank + 1) / S);
-  const int c_beg = (int)((long long)(K / GV_CHUNK) * rank / S) + warp;
+  const int wrow0 = GROUPED ? e * N : 0;                   // the expert's first row of QW and W_L
+  const int sblk0 = GROUPED ? e * ((N + 127) / 128) : 0;   // and 128-row block of SW
+  int stage = 0;                                           // of the next item to use
+  uint32_t parity = 0;                                     // of its barrier
+  bool dead = false;                                       // a wait ran out
 
   for (int tile0 = GROUPED ? 0 : blockIdx.y * p.mt;;) {
     // ---- this pass's tokens: at most mt rows
@@ -269,282 +263,433 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 2) gemv_kernel(GemvParams p) {
       tile0 = s_slot[1];
       if (nt_rows == 0) break;
     } else {
-      nt_rows = min(p.mt, n_rows - tile0);
+      nt_rows = min(p.mt, p.M - tile0);
     }
     auto xrow = [&](int m) -> const uint16_t* {
       if constexpr (GROUPED) return p.X + (size_t)(s_list[m] / p.fan) * K;
       else return p.X + (size_t)(tile0 + m) * K;
     };
 
-    auto load = [&](int c, int stage) {
-      const uint32_t sw = swarp + stage * sm.stage;
-#pragma unroll
-      for (int i = 0; i < GV_WBYTES / 512; ++i) {
-        const int lr = i * 8 + g;                         // row of the unit; its 16-byte piece t
-        const int n = row0 + i * 32 + g;
-        const bool ok = n < N;
-        cp_async16(sw + lr * 64 + ((t ^ ((lr >> 1) & 3)) << 4),
-                   QW + (size_t)(ok ? n : 0) * (K / 2) + (size_t)c * (GV_CHUNK / 2) + t * 16, ok);
-      }
-      constexpr int ATOMS = 32 / V;
-      if (lane < 8 * ATOMS)
-        cp_async16(sw + GV_WBYTES + lane * 16,
-                   SW + ((size_t)(unit >> 2) * nslot4 + (size_t)c * ATOMS + (lane >> 3)) * 512 + (unit & 3) * 128 +
-                       (lane & 7) * 16, true);
-      const uint32_t sx = sw + GV_WBYTES + GV_ROWS * 4 * ATOMS;
-      for (int i = lane; i < nt_rows * 16; i += 32) {
-        const int m = i >> 4, q = i & 15;
-        cp_async16(sx + m * 256 + ((q ^ ((m & 1) << 2)) << 4), xrow(m) + (size_t)c * GV_CHUNK + q * 8, true);
+    // ---- start the weight stream: the next item to load is pj of unit pu. Items 0 .. nc - 1 of a
+    // unit are codes; the W_L columns' items follow, known only after the table has been read.
+    const int u_step = n_cta * (NW >> p.tw_shift);
+    int items = 0x7FFFFFFF, w0 = 0;
+    int pu = dead ? p.n_units : cta + team * n_cta, poff = 0, pj = twarp;
+    auto settle = [&] {                                    // past the end of a unit: to the next one
+      while (pj >= items && pu < p.n_units) {
+        pu += u_step;
+        poff += items;
+        pj = (twarp - poff) & (tw - 1);
       }
     };
-
-#pragma unroll
-    for (int i = 0; i < ST; ++i) {
-      if (c_beg + i * GV_WARPS < c_end) load(c_beg + i * GV_WARPS, i);
-      cp_async_commit();
+    auto load_next = [&](int to) {
+      if (pu >= p.n_units) return;
+      if (lane == 0) {
+        const uint32_t sw = sbase + swarp + to * sm.stage, bar = bars + to * 8;
+        const bool main = pj < nc;
+        const CUtensorMap* const m = main ? &maps.w : &maps.wl;
+        const int x = main ? (c0 + pj) * RB : (w0 + pj - nc) * COLS;
+        mbar_arrive_expect_tx(bar, main ? GV_ROWS * RB + SBYTES : GV_ROWS * RB);
+        // octet q: rows 32 q + 8 (pu % 4) .. + 7 of the 128-row block
+        if (p.rows32) {
+          tma_load_3d(sw, m, x, (pu & 3) * 8, (wrow0 >> 5) + (pu >> 2) * 4, bar);
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q)
+            tma_load_3d(sw + q * 8 * RB, m, x, wrow0 + (pu >> 2) * 128 + q * 32 + (pu & 3) * 8, 0, bar);
+        }
+        if (main) tma_load_3d(sbase + sscale + to * SBYTES, &maps.s, (pu & 3) * 32, (c0 + pj) * (CH / V / 4), sblk0 + (pu >> 2), bar);
+      }
+      pj += tw;
+      if (pj >= items) settle();
+    };
+    const int8_t l_first = tid < n_table ? L[tid] : -1;    // on its way before the bulk of the data
+    int pre = 0;
+    int pstage = stage;
+#pragma unroll 1
+    for (; pre < ST && pj < nc; ++pre) {
+      load_next(pstage);
+      pstage = pstage + 1 == ST ? 0 : pstage + 1;
     }
 
-    float acc[2][NT][4];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
+    // the tokens, as they are: each warp copies the items it will convert
+    constexpr int XB = CH / 16;                            // bytes of a lane
+    for (int c = warp; c < nc; c += NW)
+#pragma unroll 4
+      for (int m = 0; m < nt_rows; ++m)
+        cp_async<XB>(sbase + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6)),
+                     xrow(m) + (size_t)(c0 + c) * CH + lane * (CH / 32));
 
-    // ---- protected channels: 32 columns of W_L at a time
-    for (int cc = rank * GV_WARPS + warp; cc * 32 < n_col; cc += S * GV_WARPS) {
-      const int i0 = cc * 32 + t * 8;
-      uint4 wl[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = row0 + q * 32 + g;
-        wl[q] = n < N && i0 < p.K_L ? __ldg(reinterpret_cast<const uint4*>(WL + (size_t)n * p.K_L + i0)) : make_uint4(0, 0, 0, 0);
+    // ---- the table: each entry with its W_L column (-1: none)
+    int* const ent = reinterpret_cast<int*>(smem + sm.ent);
+    int cols = 0;
+    if (n_table) {
+      const int e0 = (c0 * CH >> p.g_shift) * p.R, e1 = ((c0 + nc) * CH >> p.g_shift) * p.R;
+      int n_col = 0, it = 0;
+      for (int i = tid; i < p.mt * sm.bcols / 8; i += THREADS) reinterpret_cast<uint4*>(smem + sm.b)[i] = make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < n_table; b += THREADS, it ^= 1) {
+        const int i = b + tid;
+        int v = b == 0 ? (int)l_first : i < n_table ? (int)L[i] : -1;
+        if (v >= p.G) {
+          if (blockIdx.x == 0) record_status(p.status, DEV_BAD_TABLE);
+          v = -1;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, v >= 0);
+        if (lane == 0) s_scan[it][warp] = __popc(m);
+        __syncthreads();
+        const int c = lane < NW ? s_scan[it][lane] : 0;
+        const int col = n_col + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(m & ((1u << lane) - 1u));
+        n_col += __reduce_add_sync(0xffffffffu, c);
+        if (i == e0) s_cols[0] = col;
+        if (i == e1) s_cols[1] = col;
+        if (v >= 0 && col >= p.K_L) {
+          if (blockIdx.x == 0) record_status(p.status, DEV_BAD_TABLE);
+          v = -1;
+        }
+        if (i < n_table) ent[i] = v >= 0 ? col << 8 | v : -1;
       }
-      uint32_t xb[NT][4];
+      if (tid == 0 && e1 == n_table) s_cols[1] = n_col;
+      __syncthreads();
+      w0 = min(s_cols[0], p.K_L) / COLS;
+      cols = max(0, (min(s_cols[1], p.K_L) + COLS - 1) / COLS - w0);
+    }
+    items = nc + cols;
+    if (pj >= items) settle();
+#pragma unroll 1
+    for (; pre < ST; ++pre) {
+      load_next(pstage);
+      pstage = pstage + 1 == ST ? 0 : pstage + 1;
+    }
+
+    // ---- stage the tokens: protected channels apart, the rest as f16 with a power of two per token and item,
+    // in place (16-byte pieces of odd tokens trade places in fours, so that two tokens' 64 bytes meet
+    // different banks)
+    cp_async_wait_all();
+    for (int c = warp; c < nc; c += NW) {
+      const int k = (c0 + c) * CH + lane * (CH / 32);
+      const int grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
+      // the lane's channels that are protected, by table slot: place in the lane's run and W_L column
+      int at[MAX_R], col[MAX_R];
 #pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        const int m = b * 8 + g;
+      for (int r = 0; r < MAX_R; ++r) {
+        at[r] = -1;
+        if (n_table && r < p.R) {
+          const int w = ent[grp + r], a = (w & 255) - local;
+          if (w >= 0 && a >= 0 && a < CH / 32) { at[r] = a; col[r] = w >> 8; }
+        }
+      }
+      constexpr int MB = 4;                                  // tokens at a time, for their latencies' sake
+      for (int m0 = 0; m0 < nt_rows; m0 += MB) {
+        uint32_t v[MB][XB / 4], am[MB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t lo = 0, hi = 0;
-          const int k0 = chan[i0 + 2 * i], k1 = chan[i0 + 2 * i + 1];
-          if (m < nt_rows) {
-            const uint16_t* x = xrow(m);
-            if (k0 >= 0) lo = x[k0];
-            if (k1 >= 0) hi = x[k1];
+        for (int y = 0; y < MB; ++y) {
+          const int m = min(m0 + y, nt_rows - 1);
+          const uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+          if constexpr (XB == 8) {
+            const uint2 q = *reinterpret_cast<const uint2*>(x);
+            v[y][0] = q.x; v[y][1] = q.y;
+          } else {
+            const uint4 q = *reinterpret_cast<const uint4*>(x);
+            v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
           }
-          xb[b][i] = lo | (hi << 16);
+        }
+#pragma unroll
+        for (int r = 0; r < MAX_R; ++r)
+          if (at[r] >= 0) {
+#pragma unroll
+            for (int y = 0; y < MB; ++y) {
+              // in table order: a channel named twice gives its value once and then 0
+              const int m = m0 + y;
+              uint32_t w = 0;
+#pragma unroll
+              for (int i = 0; i < XB / 4; ++i) {
+                const uint32_t hit = i == at[r] >> 1 ? 0xFFFFu << (at[r] & 1) * 16 : 0u;
+                w |= v[y][i] & hit;
+                v[y][i] &= ~hit;
+              }
+              if (m < nt_rows)
+                *reinterpret_cast<uint16_t*>(smem + sm.b + m * sm.bcols * 2 + (((col[r] >> 3) ^ ((m & 1) << 2)) << 4) +
+                                             (col[r] & 7) * 2) = (uint16_t)(w >> (at[r] & 1) * 16);
+            }
+          }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < MB; ++y) {
+          am[y] = 0;
+#pragma unroll
+          for (int i = 0; i < XB / 4; ++i) am[y] = max(am[y], max(v[y][i] & 0x7FFFu, (v[y][i] >> 16) & 0x7FFFu));
+        }
+#pragma unroll
+        for (int y = 0; y < MB; ++y) am[y] = max(__reduce_max_sync(0xffffffffu, am[y]) >> 7, 15u);
+#pragma unroll
+        for (int y = 0; y < MB; ++y) {
+          const int m = m0 + y;
+          if (m >= nt_rows) continue;
+          const float f = __uint_as_float((268u - am[y]) << 23);   // the maximum comes to [2^14, 2^15)
+#pragma unroll
+          for (int i = 0; i < XB / 4; ++i)
+            v[y][i] = pack_f16x2(__uint_as_float(v[y][i] << 16) * f, __uint_as_float(v[y][i] & 0xFFFF0000u) * f);
+          uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+          if constexpr (XB == 8) *reinterpret_cast<uint2*>(x) = make_uint2(v[y][0], v[y][1]);
+          else *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
+          if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
         }
       }
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = 0; b < NT; ++b) {
-          mma_bf16(acc[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, xb[b][0], xb[b][1]);
-          mma_bf16(acc[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, xb[b][2], xb[b][3]);
-        }
     }
+    __syncthreads();
 
-    // ---- the 4-bit part
-    int stage = 0;
-    for (int c = c_beg; c < c_end; c += GV_WARPS) {
-      // the lane's four channels of the chunk, without the protected ones
-      uint2 keep = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
-      if (n_table) {
-        const int k = c * GV_CHUNK + lane * 4;
-        const int grp = k / p.G, local = k - grp * p.G;
-        for (int r = 0; r < p.R; ++r) {
-          const int at = (int)L[grp * p.R + r] - local;
-          if (at == 0) keep.x &= 0xFFFF0000u;
-          if (at == 1) keep.x &= 0x0000FFFFu;
-          if (at == 2) keep.y &= 0xFFFF0000u;
-          if (at == 3) keep.y &= 0x0000FFFFu;
-        }
+    // ---- the units
+    // B operand: lane (g, t) reads token g of each tile; lanes past the last token repeat it (their
+    // products land in columns that are never stored)
+    int xa[NT], ba[NT];
+#pragma unroll
+    for (int b = 0; b < NT; ++b) {
+      const int m = min(b * 8 + g, nt_rows - 1);
+      xa[b] = sm.x + m * p.kc * 2 + ((m & 1) << 6) + (V == 32 ? t * 16 : (t >> 1) * 16 + (t & 1) * 8);
+      ba[b] = sm.b + m * sm.bcols * 2 + ((m & 1) << 6) + t * 16;
+    }
+    const int rsw = CH == 256 ? g : (g >> 1) & 3;           // swizzle of the lane's row in each octet
+    const int rd = g * RB + (rsw << 4) + t * (V == 32 ? 4 : 2), rw = g * RB + ((rsw ^ t) << 4);   // codes, W_L
+    auto next_stage = [&] {
+      if (++stage == ST) {
+        stage = 0;
+        parity ^= 1;
       }
-      cp_async_wait<ST - 1>();
-      __syncwarp();
-      const uint32_t sw = swarp + stage * sm.stage;
-      const uint32_t ss = sw + GV_WBYTES;
-      const uint32_t sx = ss + GV_ROWS * 4 * (32 / V);
-      const uint32_t sf = sx + p.mt * 256;
-      // tokens to f16, in place
-      for (int m = 0; m < nt_rows; ++m) {
-        const uint32_t a = sx + m * 256 + (((lane >> 1) ^ ((m & 1) << 2)) << 4) + (lane & 1) * 8;
-        uint2 v = lds64(a);
-        v.x &= keep.x;
-        v.y &= keep.y;
-        const uint32_t am = max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
-        const uint32_t ex = max(redux_max(am) >> 7, 15u);
-        const float f = __uint_as_float((268u - ex) << 23);    // the maximum comes to [2^14, 2^15)
-        v.x = pack_f16x2(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xFFFF0000u) * f);
-        v.y = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xFFFF0000u) * f);
-        sts64(a, v);
-        if (lane == 0) sts32f(sf + m * 4, __uint_as_float((ex - 14u) << 23));
-      }
-      __syncwarp();
-      float cs[2][NT][4];
+    };
+    int off = 0;
+    int red = sm.red;                                        // this unit's set of sums (NT = 1)
+    for (int u = cta + team * n_cta; u < p.n_units; u += u_step) {
+      float acc[2][NT][4];
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) cs[a][b][i] = 0.f;
-      uint4 sc[32 / V];                                        // this row's scale words, octets 0..3
-#pragma unroll
-      for (int i = 0; i < 32 / V; ++i) sc[i] = lds128(ss + i * 128 + g * 16);
-#pragma unroll
-      for (int blk = 0; blk < 4; ++blk) {
-        uint32_t xb[NT][4];
-#pragma unroll
-        for (int b = 0; b < NT; ++b) {
-          const int m = b * 8 + g;
-          const uint32_t a = sx + m * 256;
-          const int sz = (m & 1) << 2;
-          if (m < nt_rows) {
-            if constexpr (V == 32) {
-              const uint4 v = lds128(a + (((blk * 4 + t) ^ sz) << 4));
-              xb[b][0] = v.x; xb[b][1] = v.y; xb[b][2] = v.z; xb[b][3] = v.w;
-            } else {
-              const uint2 u = lds64(a + (((blk * 4 + (t >> 1)) ^ sz) << 4) + (t & 1) * 8);
-              const uint2 v = lds64(a + (((blk * 4 + 2 + (t >> 1)) ^ sz) << 4) + (t & 1) * 8);
-              xb[b][0] = u.x; xb[b][1] = u.y; xb[b][2] = v.x; xb[b][3] = v.y;
-            }
-          } else {
-            xb[b][0] = xb[b][1] = xb[b][2] = xb[b][3] = 0u;
-          }
+          for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
+      const int j0 = (twarp - off) & (tw - 1);
+      for (int j = j0; j < items; j += tw) {
+        // a wait that ran out is recorded: nothing more is loaded, every loop ends, the sums are undefined
+        if (!mbar_wait(bars + stage * 8, parity, &s_abort, p.status)) {
+          dead = true;
+          pu = p.n_units;
         }
+        const int sw = swarp + stage * sm.stage;
+        if (j >= nc) {
+          // protected channels: COLS columns of W_L
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const int lo = a * 16 + g, hi = lo + 8;
-          const uint32_t al = sw + lo * 64 + ((blk ^ ((lo >> 1) & 3)) << 4), ah = sw + hi * 64 + ((blk ^ ((hi >> 1) & 3)) << 4);
-          uint32_t wl, wh;
-          if constexpr (V == 32) {
-            wl = lds32(al + t * 4);
-            wh = lds32(ah + t * 4);
-          } else {
-            wl = lds16(al + t * 2) | (lds16(al + 8 + t * 2) << 16);
-            wh = lds16(ah + t * 2) | (lds16(ah + 8 + t * 2) << 16);
-          }
-          uint32_t fl[4], fh[4];
-          e2m1x8_to_f16(wl, fl);
-          e2m1x8_to_f16(wh, fh);
-          if constexpr (V == 32) {
-            const uint32_t wdl = a == 0 ? sc[0].x : sc[0].z, wdh = a == 0 ? sc[0].y : sc[0].w;
-            const float s0 = e8m0((wdl >> (8 * blk)) & 255u), s1 = e8m0((wdh >> (8 * blk)) & 255u);
+          for (int h = 0; h < CH / 128; ++h) {
+            uint4 wl[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wl[q] = ld128(((sw + rw) ^ (h * 64)) + q * 8 * RB);
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(d, fl[0], fh[0], fl[1], fh[1], xb[b][0], xb[b][1]);
-              mma_f16(d, fl[2], fh[2], fl[3], fh[3], xb[b][2], xb[b][3]);
-              cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
-              cs[a][b][1] = fmaf(d[1], s0, cs[a][b][1]);
-              cs[a][b][2] = fmaf(d[2], s1, cs[a][b][2]);
-              cs[a][b][3] = fmaf(d[3], s1, cs[a][b][3]);
-            }
-          } else {
+              const int c = (w0 + j - nc) * (COLS / 32) + h;
+              const uint4 x = ld128((ba[b] + (c >> 1) * 128) ^ ((c & 1) * 64));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int slot = blk * 2 + h;
-              const uint4 w4 = sc[slot >> 2];
-              const uint32_t wdl = a == 0 ? w4.x : w4.z, wdh = a == 0 ? w4.y : w4.w;
-              const float s0 = e8m0((wdl >> (8 * (slot & 3))) & 255u), s1 = e8m0((wdh >> (8 * (slot & 3))) & 255u);
-#pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, fl[2 * h], fh[2 * h], fl[2 * h + 1], fh[2 * h + 1], xb[b][2 * h], xb[b][2 * h + 1]);
-                cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
-                cs[a][b][1] = fmaf(d[1], s0, cs[a][b][1]);
-                cs[a][b][2] = fmaf(d[2], s1, cs[a][b][2]);
-                cs[a][b][3] = fmaf(d[3], s1, cs[a][b][3]);
+              for (int a = 0; a < 2; ++a) {
+                mma_bf16(acc[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, x.x, x.y);
+                mma_bf16(acc[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, x.z, x.w);
               }
             }
           }
+        } else {
+          float cs[2][NT][4];
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) cs[a][b][i] = 0.f;
+#pragma unroll
+          for (int h = 0; h < CH / 128; ++h) {
+            float sc[4][4 * SLOT];                                 // scales of the lane's row in octets 0..3
+#pragma unroll
+            for (int i = 0; i < SLOT; ++i) {
+              const uint4 w = ld128(sscale + stage * SBYTES + (h * SLOT + i) * 128 + g * 16);
+              e8m0x4(w.x, reinterpret_cast<float(&)[4]>(sc[0][4 * i]));
+              e8m0x4(w.y, reinterpret_cast<float(&)[4]>(sc[1][4 * i]));
+              e8m0x4(w.z, reinterpret_cast<float(&)[4]>(sc[2][4 * i]));
+              e8m0x4(w.w, reinterpret_cast<float(&)[4]>(sc[3][4 * i]));
+            }
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+              uint32_t xb[NT][4];
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                const int x = ((xa[b] + j * (CH * 2)) ^ (blk * 64)) + h * 256;
+                if constexpr (V == 32) {
+                  const uint4 v = ld128(x);
+                  xb[b][0] = v.x; xb[b][1] = v.y; xb[b][2] = v.z; xb[b][3] = v.w;
+                } else {
+                  const uint2 u2 = ld64(x), v = ld64(x + 32);
+                  xb[b][0] = u2.x; xb[b][1] = u2.y; xb[b][2] = v.x; xb[b][3] = v.y;
+                }
+              }
+              const int w = (sw + rd) ^ ((h * 4 + blk) * 16);
+#pragma unroll
+              for (int a = 0; a < 2; ++a) {
+                const int lo = w + a * 16 * RB, hi = lo + 8 * RB;
+                uint32_t wl, wh;
+                if constexpr (V == 32) {
+                  wl = ld32(lo);
+                  wh = ld32(hi);
+                } else {
+                  wl = ld16(lo) | (ld16(lo + 8) << 16);
+                  wh = ld16(hi) | (ld16(hi + 8) << 16);
+                }
+                uint32_t fl[4], fh[4];
+                e2m1x8_to_f16(wl, fl);
+                e2m1x8_to_f16(wh, fh);
+#pragma unroll
+                for (int y = 0; y < SLOT; ++y) {
+                  const float s0 = sc[2 * a][blk * SLOT + y], s1 = sc[2 * a + 1][blk * SLOT + y];
+#pragma unroll
+                  for (int b = 0; b < NT; ++b) {
+                    float d[4];
+                    mma_f16_first(d, fl[2 * y], fh[2 * y], fl[2 * y + 1], fh[2 * y + 1], xb[b][2 * y], xb[b][2 * y + 1]);
+                    if constexpr (V == 32) mma_f16(d, fl[2], fh[2], fl[3], fh[3], xb[b][2], xb[b][3]);
+                    cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
+                    cs[a][b][1] = fmaf(d[1], s0, cs[a][b][1]);
+                    cs[a][b][2] = fmaf(d[2], s1, cs[a][b][2]);
+                    cs[a][b][3] = fmaf(d[3], s1, cs[a][b][3]);
+                  }
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < NT; ++b) {
+            const uint2 f = ld64(sm.xs + (j * 8 * NT + b * 8 + 2 * t) * 4);
+            const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              acc[a][b][0] = fmaf(cs[a][b][0], f0, acc[a][b][0]);
+              acc[a][b][1] = fmaf(cs[a][b][1], f1, acc[a][b][1]);
+              acc[a][b][2] = fmaf(cs[a][b][2], f0, acc[a][b][2]);
+              acc[a][b][3] = fmaf(cs[a][b][3], f1, acc[a][b][3]);
+            }
+          }
+        }
+        if (NT == 1 || j + tw < items) {                     // NT = 2: the last stage takes the sums first
+          __syncwarp();
+          load_next(stage);
+          next_stage();
         }
       }
-#pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        const int m = b * 8 + 2 * t;
-        const float f0 = m < nt_rows ? lds32f(sf + m * 4) : 0.f, f1 = m + 1 < nt_rows ? lds32f(sf + m * 4 + 4) : 0.f;
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          acc[a][b][0] = fmaf(cs[a][b][0], f0, acc[a][b][0]);
-          acc[a][b][1] = fmaf(cs[a][b][1], f1, acc[a][b][1]);
-          acc[a][b][2] = fmaf(cs[a][b][2], f0, acc[a][b][2]);
-          acc[a][b][3] = fmaf(cs[a][b][3], f1, acc[a][b][3]);
-        }
-      }
-      __syncwarp();
-      if (c + ST * GV_WARPS < c_end) load(c + ST * GV_WARPS, stage);
-      cp_async_commit();
-      stage = stage + 1 == ST ? 0 : stage + 1;
-    }
-    cp_async_wait<0>();
-    __syncwarp();
 
-    // ---- join the warps' sums (each in its own first stage), then the cluster's, in rank order
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
+      // ---- join the team's sums (every warp has had an item): in one of two sets (the other may still
+      // be being read), or where these do not fit (NT = 2) in the stage just consumed
+      int* const at = reinterpret_cast<int*>(smem + sm.at);
+      int to = red + warp * gv_sums(NT);
+      if constexpr (NT == 2) {
+        __syncwarp();
+        to = swarp + stage * sm.stage;
+        if (lane == 0) at[warp] = to;
+      }
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int lr = a * 16 + g + (i >> 1) * 8, m = b * 8 + 2 * t + (i & 1);
-          sts32f(swarp + (m * GV_ROWS + lr) * 4, acc[a][b][i]);
+        for (int i = 0; i < 2; ++i) {
+          const int m = b * 8 + 2 * t + i;
+          if (m >= nt_rows) continue;
+          float* const x = reinterpret_cast<float*>(smem + to) + m * GV_PITCH + g;
+          x[0] = acc[0][b][i];
+          x[8] = acc[0][b][2 + i];
+          x[16] = acc[1][b][i];
+          x[24] = acc[1][b][2 + i];
         }
-    __syncthreads();
-    const int n_out = nt_rows * GV_ROWS;
-    auto store = [&](int o, float v) {
-      const int m = o / GV_ROWS, lr = o % GV_ROWS;
-      const int n = row0 + (lr >> 3) * 32 + (lr & 7);
-      if (n >= N) return;
-      size_t r;
-      if constexpr (GROUPED) r = (size_t)s_list[m];
-      else r = (size_t)(tile0 + m);
-      __nv_bfloat16 h = __float2bfloat16_rn(v);
-      p.Y[r * N + n] = *reinterpret_cast<uint16_t*>(&h);
-      if (p.Yf32) p.Yf32[r * N + n] = v;
-    };
-    for (int o = tid; o < n_out; o += GV_WARPS * 32) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < GV_WARPS; ++w) v += lds32f(sbase + w * sm.warp + o * 4);
-      if (S == 1) store(o, v);
-      else s_sum[o] = v;
-    }
-    if (S > 1) {
-      cluster_sync();
-      const uint32_t su = smem_u32(s_sum);
-      for (int o = tid * S + rank; o < n_out; o += GV_WARPS * 32 * S) {
+      if (NT == 2) fence_proxy_async_smem();                 // the next copy into this stage comes after
+      team_sync(1 + team, tw * 32);
+      const int row0 = (u >> 2) * 128 + (u & 3) * 8;
+      auto store = [&](int m, int lr, float v) {
+        const int n = row0 + (lr >> 3) * 32 + (lr & 7);
+        if (n >= N) return;
+        size_t r;
+        if constexpr (GROUPED) r = (size_t)s_list[m];
+        else r = (size_t)(tile0 + m);
+        __nv_bfloat16 h = __float2bfloat16_rn(v);
+        p.Y[r * N + n] = *reinterpret_cast<uint16_t*>(&h);
+        if (p.Yf32) p.Yf32[r * N + n] = v;
+      };
+      // a warp sums a token's 32 rows over the team, another warp's turn first in each unit
+      for (int m = j0; m < nt_rows; m += tw) {
         float v = 0.f;
-        for (int r = 0; r < S; ++r) v += lds32f_cluster(mapa_shared(su + o * 4, r));
-        store(o, v);
+#pragma unroll 8
+        for (int w = team * tw; w < team * tw + tw; ++w) {
+          const int from = NT == 1 ? red + w * gv_sums(NT) : at[w];
+          v += reinterpret_cast<const float*>(smem + from)[m * GV_PITCH + lane];
+        }
+        if (S == 1) store(m, lane, v);
+        else s_sum[m * GV_ROWS + lane] = v;
       }
-      cluster_sync();                                      // the others have read this CTA's sums
+      if (S > 1) {                                           // one team per CTA
+        cluster_sync();
+        const uint32_t su = smem_u32(s_sum);
+        for (int o = tid * S + rank; o < nt_rows * GV_ROWS; o += THREADS * S) {
+          float v = 0.f;
+          for (int r = 0; r < S; ++r) v += lds32f_cluster(mapa_shared(su + o * 4, r));
+          store(o / GV_ROWS, o % GV_ROWS, v);
+        }
+        cluster_sync();                                      // the others have read this CTA's sums
+      } else if (NT == 2) {
+        team_sync(1 + team, tw * 32);                        // the sums have been read
+      }
+      if (NT == 2) {
+        load_next(stage);
+        next_stage();
+      }
+      if (NT == 1) red = 2 * sm.red + NW * gv_sums(NT) - red;
+      off += items;
     }
     if constexpr (!GROUPED) break;
-    __syncthreads();                                       // the list and the stages are free again
+    __syncthreads();                                         // the list and the tokens are free again
+  }
+  // after a timeout, copies still in flight get a moment to land before the shared memory is given up
+  if (*reinterpret_cast<volatile int*>(&s_abort)) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 10000000ull) {}
   }
 }
 
 namespace {
 
-template <int V, int NT, int ST, bool GROUPED>
-cudaError_t launch_t(GemvParams p, int slots, cudaStream_t s) {
+// Tensor maps of the weight's parts, one copy of an item each. Rows as (32 rows) x (blocks of 32), so
+// that one box {a row's bytes, 8 rows, 4 blocks} is a unit's four octets; where N is not a multiple of
+// 32 as one run of rows, a box of 8. Swizzled by the row length, so that 8 rows' equal pieces meet
+// different banks. Scales as (128 words of an atom) x (atoms along K) x (128-row blocks).
+cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int V, int CH, int E) {
+  const uint64_t rows = (uint64_t)E * p.N;
+  const CUtensorMapSwizzle sw = CH == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  auto operand = [&](CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t width, uint64_t pitch, uint32_t box) {
+    const uint64_t d3[3] = {width, 32, rows / 32}, s3[2] = {pitch, pitch * 32};
+    const uint64_t d1[3] = {width, rows, 1}, s1[2] = {pitch, pitch * rows};
+    const uint32_t b3[3] = {box, 8, 4}, b1[3] = {box, 8, 1};
+    return p.rows32 ? encode_map(map, dt, 3, base, d3, s3, b3, sw) : encode_map(map, dt, 3, base, d1, s1, b1, sw);
+  };
+  cudaError_t e = operand(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.QW, (uint64_t)p.K / 2, (uint64_t)p.K / 2, CH / 2);
+  if (e == cudaSuccess && p.L && p.K_L)
+    e = operand(&m->wl, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.WL, (uint64_t)p.K_L, (uint64_t)p.K_L * 2, CH / 4);
+  const uint64_t atoms = (uint64_t)p.K / V / 4;
+  const uint64_t d[3] = {128, atoms, (uint64_t)E * ((p.N + 127) / 128)}, st[2] = {512, atoms * 512};
+  const uint32_t box[3] = {32, (uint32_t)(CH / V / 4), 1};
+  if (e == cudaSuccess) e = encode_map(&m->s, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, p.SW, d, st, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return e;
+}
+
+constexpr int GV_SMEM_MAX = 232448 - 8192;                   // 227 KB less the static part and a reserve
+
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, int slots, int n_cta, cudaStream_t s) {
   static PerDeviceOnce attr_once;
   const cudaError_t ae = attr_once.run([] {
-    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<V, NT, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
-    return e;
+    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                GV_SMEM_MAX);
   });
   if (ae != cudaSuccess) return ae;
-  const int n_table = p.L ? p.K / p.G * p.R : 0;
-  const int per_cta = (p.K / GV_CHUNK + p.S - 1) / p.S;
-  p.stages = std::min(ST, (per_cta + GV_WARPS - 1) / GV_WARPS);
-  const GvSmem sm = gv_smem(V, p.mt, p.stages, std::min(n_table, p.K_L), GROUPED ? p.M : 0, GROUPED ? p.E : 0);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.n_units * p.S, slots, 1);
-  cfg.blockDim = dim3(GV_WARPS * 32, 1, 1);
-  cfg.dynamicSmemBytes = sm.total;
+  cfg.gridDim = dim3(n_cta * p.S, slots, 1);
+  cfg.blockDim = dim3(NW * 32, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -555,38 +700,76 @@ cudaError_t launch_t(GemvParams p, int slots, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, NT, ST, GROUPED>, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED>, maps, p);
 }
 
-template <int NT, int ST, bool GROUPED>
-cudaError_t launch_v(const GemvParams& p, int slots, cudaStream_t s) {
-  return p.G == 16 ? launch_t<16, NT, ST, GROUPED>(p, slots, s) : launch_t<32, NT, ST, GROUPED>(p, slots, s);
+// The split of one call. CH, NT, NW and ST are the kernel's, mt the tokens of a pass.
+template <int CH, int NT, int NW, int ST, bool GROUPED>
+cudaError_t launch_v(GemvParams p, int slots, int num_sms, cudaStream_t s) {
+  static const int tw_min = getenv("TWM") ? atoi(getenv("TWM")) : 4, tw_units = getenv("TWU") ? atoi(getenv("TWU")) : 2;
+  const int V = p.G == 16 ? 16 : 32;
+  const int chunks = p.K / CH;
+  const int n_table = p.L ? p.K / p.G * p.R : 0;
+  GemvMaps maps;
+  cudaError_t e = encode_gemv_maps(&maps, p, V, CH, GROUPED ? p.E : 1);
+  if (e != cudaSuccess) return e;
+  auto smem_of = [&](int S) {
+    p.kc = (chunks + S - 1) / S * CH;
+    return gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
+  };
+  // parts of K: enough for the tokens to fit, and to fill the SMs where units are few
+  p.S = std::max(1, std::min({8, num_sms / std::max(1, p.n_units * slots), chunks / NW}));
+  while (smem_of(p.S) > GV_SMEM_MAX) {
+    if (p.S < 8 && chunks / (p.S + 1) >= NW) ++p.S;
+    else if (p.mt > 1) p.mt = (p.mt + 1) / 2;
+    else return cudaErrorInvalidValue;
+  }
+  const int smem = smem_of(p.S);
+  p.nc_base = chunks / p.S;
+  p.nc_more = chunks % p.S;
+  // every warp of a team has an item of every unit; a cluster's CTAs are one team each
+  int tw = NW;
+  if (p.S == 1)
+    while (tw > chunks || (tw > tw_min && p.n_units >= tw_units * num_sms * NW / tw)) tw /= 2;
+  p.tw_shift = 0;
+  while ((1 << p.tw_shift) < tw) ++p.tw_shift;
+  const int per_sm = std::max(1, std::min(2048 / 32 / NW / 2, 232448 / (smem + 4096)));
+  const int teams = NW / tw;
+  int n_cta = std::max(1, per_sm * num_sms / p.S);
+  if (GROUPED) {
+    slots = std::min(p.M, p.E);
+    n_cta = std::max(1, (2 * per_sm * num_sms / p.S + slots - 1) / slots);
+  } else {
+    slots = (p.M + p.mt - 1) / p.mt;
+  }
+  n_cta = std::min(n_cta, (p.n_units + teams - 1) / teams);
+  p.n_cta = n_cta;
+  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s)
+                 : launch_t<32, CH, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
-  (void)num_sms;
   GemvParams p = q;
   p.n_units = p.N / 128 * 4 + std::min(4, p.N % 128 / 8);
-  const int chunks = p.K / GV_CHUNK;
-  // the K range of a CTA: at most 4 chunks per warp
-  p.S = std::max(1, std::min(8, (chunks + 4 * GV_WARPS - 1) / (4 * GV_WARPS)));
+  p.g_shift = p.G == 16 ? 4 : p.G == 32 ? 5 : 6;
+  p.rows32 = p.N % 32 == 0;
   if (p.expert) {
     const int slots = std::min(p.M, p.E);
     if (p.M <= 64) {
       p.mt = std::min(p.M, 8);
-      return launch_v<1, 4, true>(p, slots, s);
+      return launch_v<256, 1, 8, 2, true>(p, slots, num_sms, s);
     }
     p.mt = 16;
-    return launch_v<2, 2, true>(p, slots, s);
+    return launch_v<256, 2, 8, 2, true>(p, slots, num_sms, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    return launch_v<1, 4, false>(p, 1, s);
+    return launch_v<256, 1, 16, 2, false>(p, 1, num_sms, s);
   }
   p.mt = std::min(p.M, 16);
-  return launch_v<2, 2, false>(p, (p.M + 15) / 16, s);
+  return launch_v<256, 2, 8, 2, false>(p, 1, num_sms, s);
 }
 
 }  // namespace osc

@@ -102,8 +102,14 @@ struct GemvParams {
   const int* expert;       // grouped: M expert ids (device); nullptr = dense
   int fan, E;              // grouped: row r reads X row r / fan
   // set by the launcher
-  int S, n_units, mt, stages;
+  int S, n_cta, n_units, mt, kc, nc_base, nc_more, tw_shift, g_shift, rows32;
 };
+struct GemvMaps {
+  CUtensorMap w, s, wl;
+};
+// Tiled tensor map over a row-major tensor; dims[0] is the contiguous dimension (rank <= 3).
+cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 // grouped form: most rows and experts of one call (their ids are staged in shared memory)
 constexpr int GEMV_MAX_ROWS = 4096;
 constexpr int GEMV_MAX_EXPERTS = 4096;
