@@ -23,6 +23,7 @@
 // with W_L run as bf16 mma into the same sums.
 #include <cuda_fp16.h>
 #include <cstdlib>
+#include <type_traits>
 
 #include "osc_device.cuh"
 #include "osc_internal.h"
@@ -46,14 +47,35 @@ __device__ __forceinline__ float lds32f_cluster(uint32_t a) {
 }
 
 // Eight E2M1 codes (low nibble first) as four f16 pairs, exact.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& h0, uint32_t& h1, uint32_t& h2, uint32_t& h3) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "mov.b32 {a, b, c, d}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
       "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
       "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
       "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+      : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3) : "r"(w));
+}
+
+// LB bytes of codes as f16 pairs; with LB = 2 also the two 8 bytes further, the next step's.
+template <int LB>
+__device__ __forceinline__ void load_codes(const uint8_t* from, uint32_t (&h)[LB == 2 ? 4 : LB]) {
+  if constexpr (LB == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(from);
+    e2m1x8_to_f16(v.x, h[0], h[1], h[2], h[3]);
+    e2m1x8_to_f16(v.y, h[4], h[5], h[6], h[7]);
+    e2m1x8_to_f16(v.z, h[8], h[9], h[10], h[11]);
+    e2m1x8_to_f16(v.w, h[12], h[13], h[14], h[15]);
+  } else if constexpr (LB == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(from);
+    e2m1x8_to_f16(v.x, h[0], h[1], h[2], h[3]);
+    e2m1x8_to_f16(v.y, h[4], h[5], h[6], h[7]);
+  } else if constexpr (LB == 4) {
+    e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(from), h[0], h[1], h[2], h[3]);
+  } else {
+    const uint32_t lo = *reinterpret_cast<const uint16_t*>(from), hi = *reinterpret_cast<const uint16_t*>(from + 8);
+    e2m1x8_to_f16(lo | hi << 16, h[0], h[1], h[2], h[3]);
+  }
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -73,18 +95,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The four scales 2^(byte - 127) of a layout word, through bf16 (exact, 2^-127 as its subnormal).
-__device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
-      "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(w));
-  f[0] = __uint_as_float(lo << 16);
-  f[1] = __uint_as_float(lo & 0xFFFF0000u);
-  f[2] = __uint_as_float(hi << 16);
-  f[3] = __uint_as_float(hi & 0xFFFF0000u);
+// The two scales 2^(byte - 127) of the low bytes, through bf16 (exact, 2^-127 as its subnormal).
+__device__ __forceinline__ void e8m0x2(uint32_t w, float& f0, float& f1) {
+  uint32_t b;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %1;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\t}"
+      : "=r"(b) : "r"(w));
+  f0 = __uint_as_float(b << 16);
+  f1 = __uint_as_float(b & 0xFFFF0000u);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -102,7 +121,7 @@ __device__ __forceinline__ int cluster_id() {
 // Shared memory of a CTA, in bytes from its start. CH: channels of an item; kc: channels of this
 // CTA's K range (at most); cols: W_L columns.
 struct GvSmem {
-  int stage, warp, sc, x, red, xs, b, bcols, ent, ids, flag, at, total;
+  int stage, warp, sc, x, zero, red, xs, b, bcols, ent, ids, flag, at, total;
 };
 // A warp's sums, [token][row]: the row pitch of 36 floats keeps the mma fragments' stores (tokens 2t,
 // rows g) and the reads (32 rows) off each other's banks.
@@ -115,7 +134,8 @@ __host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST,
   m.warp = ST * m.stage;
   m.sc = NW * m.warp;                                              // the stages' scales
   m.x = m.sc + NW * ST * GV_ROWS * CH / V;                         // tokens in f16
-  m.red = m.x + mt * kc * 2;                                       // two sets of the warps' sums (NT = 1)
+  m.zero = m.x + mt * kc * 2;                                      // 64 bytes of zeros
+  m.red = m.zero + 64;                                       // two sets of the warps' sums (NT = 1)
   m.xs = m.red + (NT == 1 ? 2 * NW * gv_sums(NT) : 0);             // the tokens' powers of two, per item
   m.b = (m.xs + kc / CH * NT * 32 + 127) / 128 * 128;              // protected channels' values
   m.bcols = ((cols < n_table ? cols : n_table) + 63) / 64 * 64;
@@ -127,14 +147,17 @@ __host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST,
   return m;
 }
 
+// The team's warps meet at a barrier of their own (at most 8 teams of two warps or more need one).
 __device__ __forceinline__ void team_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+  if (threads == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace
 
-// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp.
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+// V: channels of a scale slot; CH: channels of an item; P: scale blocks of an mma; NT: token tiles of 8; NW: warps; ST: stages
+// per warp.
+template <int V, int CH, int P, int NT, int NW, int ST, bool GROUPED>
 __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -146,7 +169,9 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   __shared__ int s_slot[3];   // rows of this pass, where the next one starts, the expert
   __shared__ float s_sum[GV_ROWS * 8 * NT];
   constexpr int THREADS = NW * 32;
-  constexpr int SLOT = 32 / V;                             // scale slots of a 32-channel block
+  constexpr int SLOT = 32 / V;                             // scale slots of 32 channels
+  constexpr int STEP = V * P;                              // channels of a step: P scale blocks
+  constexpr int LB = STEP / 8;                             // a lane's code bytes of a step and row
   constexpr int RB = CH / 2;                               // bytes of an item's row: codes, or CH / 4 W_L columns
   constexpr int COLS = CH / 4;
   constexpr int SBYTES = GV_ROWS * CH / V;                 // scales of an item
@@ -161,7 +186,6 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   const int swarp = warp * sm.warp, sscale = sm.sc + warp * (ST * SBYTES);
   const int tw = 1 << p.tw_shift, team = warp >> p.tw_shift, twarp = warp & (tw - 1);
   auto ld32 = [&](int off) { return *reinterpret_cast<const uint32_t*>(smem + off); };
-  auto ld16 = [&](int off) { return (uint32_t)*reinterpret_cast<const uint16_t*>(smem + off); };
   auto ld64 = [&](int off) { return *reinterpret_cast<const uint2*>(smem + off); };
   auto ld128 = [&](int off) { return *reinterpret_cast<const uint4*>(smem + off); };
   // this CTA's part of K, in items
@@ -169,6 +193,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
 
   // a warp's stages and their barriers are its own
   const uint32_t bars = smem_u32(&s_full[warp][0]);
+  if (tid < 16) reinterpret_cast<uint32_t*>(smem + sm.zero)[tid] = 0u;
   if (lane == 0) {
     s_abort = 0;
     for (int i = 0; i < ST; ++i) mbar_init(bars + i * 8, 1);
@@ -304,14 +329,6 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       if (pj >= items) settle();
     };
     const int8_t l_first = tid < n_table ? L[tid] : -1;    // on its way before the bulk of the data
-    int pre = 0;
-    int pstage = stage;
-#pragma unroll 1
-    for (; pre < ST && pj < nc; ++pre) {
-      load_next(pstage);
-      pstage = pstage + 1 == ST ? 0 : pstage + 1;
-    }
-
     // the tokens, as they are: each warp copies the items it will convert
     constexpr int XB = CH / 16;                            // bytes of a lane
     for (int c = warp; c < nc; c += NW)
@@ -319,6 +336,14 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       for (int m = 0; m < nt_rows; ++m)
         cp_async<XB>(sbase + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6)),
                      xrow(m) + (size_t)(c0 + c) * CH + lane * (CH / 32));
+
+    int pre = 0;
+    int pstage = stage;
+#pragma unroll 1
+    for (; pre < 1 && pj < nc; ++pre) {       // one item; the others when the tokens are staged
+      load_next(pstage);
+      pstage = pstage + 1 == ST ? 0 : pstage + 1;
+    }
 
     // ---- the table: each entry with its W_L column (-1: none)
     int* const ent = reinterpret_cast<int*>(smem + sm.ent);
@@ -355,101 +380,104 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     }
     items = nc + cols;
     if (pj >= items) settle();
-#pragma unroll 1
-    for (; pre < ST; ++pre) {
-      load_next(pstage);
-      pstage = pstage + 1 == ST ? 0 : pstage + 1;
-    }
 
     // ---- stage the tokens: protected channels apart, the rest as f16 with a power of two per token and item,
     // in place (16-byte pieces of odd tokens trade places in fours, so that two tokens' 64 bytes meet
     // different banks)
     cp_async_wait_all();
-    for (int c = warp; c < nc; c += NW) {
-      const int k = (c0 + c) * CH + lane * (CH / 32);
-      const int grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
-      // the lane's channels that are protected, by table slot: place in the lane's run and W_L column
-      int at[MAX_R], col[MAX_R];
+    auto convert = [&](auto mb) {
+      constexpr int MB = decltype(mb)::value;                // tokens at a time, for their latencies' sake
+      for (int c = warp; c < nc; c += NW) {
+        const int k = (c0 + c) * CH + lane * (CH / 32);
+        const int grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
+        for (int m0 = 0; m0 < nt_rows; m0 += MB) {
+          uint32_t v[MB][XB / 4], am[MB];
 #pragma unroll
-      for (int r = 0; r < MAX_R; ++r) {
-        at[r] = -1;
-        if (n_table && r < p.R) {
-          const int w = ent[grp + r], a = (w & 255) - local;
-          if (w >= 0 && a >= 0 && a < CH / 32) { at[r] = a; col[r] = w >> 8; }
-        }
-      }
-      constexpr int MB = 4;                                  // tokens at a time, for their latencies' sake
-      for (int m0 = 0; m0 < nt_rows; m0 += MB) {
-        uint32_t v[MB][XB / 4], am[MB];
-#pragma unroll
-        for (int y = 0; y < MB; ++y) {
-          const int m = min(m0 + y, nt_rows - 1);
-          const uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
-          if constexpr (XB == 8) {
-            const uint2 q = *reinterpret_cast<const uint2*>(x);
-            v[y][0] = q.x; v[y][1] = q.y;
-          } else {
-            const uint4 q = *reinterpret_cast<const uint4*>(x);
-            v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < MAX_R; ++r)
-          if (at[r] >= 0) {
-#pragma unroll
-            for (int y = 0; y < MB; ++y) {
-              // in table order: a channel named twice gives its value once and then 0
-              const int m = m0 + y;
-              uint32_t w = 0;
-#pragma unroll
-              for (int i = 0; i < XB / 4; ++i) {
-                const uint32_t hit = i == at[r] >> 1 ? 0xFFFFu << (at[r] & 1) * 16 : 0u;
-                w |= v[y][i] & hit;
-                v[y][i] &= ~hit;
-              }
-              if (m < nt_rows)
-                *reinterpret_cast<uint16_t*>(smem + sm.b + m * sm.bcols * 2 + (((col[r] >> 3) ^ ((m & 1) << 2)) << 4) +
-                                             (col[r] & 7) * 2) = (uint16_t)(w >> (at[r] & 1) * 16);
+          for (int y = 0; y < MB; ++y) {
+            const int m = MB == 1 ? m0 : min(m0 + y, nt_rows - 1);
+            const uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+            if constexpr (XB == 8) {
+              const uint2 q = *reinterpret_cast<const uint2*>(x);
+              v[y][0] = q.x; v[y][1] = q.y;
+            } else {
+              const uint4 q = *reinterpret_cast<const uint4*>(x);
+              v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
             }
           }
-        __syncwarp();
+          if (n_table)
+            for (int r = 0; r < p.R; ++r) {
+              const int w = ent[grp + r], at = (w & 255) - local, col = w >> 8;
+              if (w < 0 || at < 0 || at >= CH / 32) continue;
 #pragma unroll
-        for (int y = 0; y < MB; ++y) {
-          am[y] = 0;
+              for (int y = 0; y < MB; ++y) {
+                // in table order: a channel named twice gives its value once and then 0
+                const int m = m0 + y;
+                uint32_t x = 0;
 #pragma unroll
-          for (int i = 0; i < XB / 4; ++i) am[y] = max(am[y], max(v[y][i] & 0x7FFFu, (v[y][i] >> 16) & 0x7FFFu));
-        }
+                for (int i = 0; i < XB / 4; ++i) {
+                  const uint32_t hit = i == at >> 1 ? 0xFFFFu << (at & 1) * 16 : 0u;
+                  x |= v[y][i] & hit;
+                  v[y][i] &= ~hit;
+                }
+                if (MB == 1 || m < nt_rows)
+                  *reinterpret_cast<uint16_t*>(smem + sm.b + m * sm.bcols * 2 + (((col >> 3) ^ ((m & 1) << 2)) << 4) +
+                                               (col & 7) * 2) = (uint16_t)(x >> (at & 1) * 16);
+              }
+            }
+          __syncwarp();
 #pragma unroll
-        for (int y = 0; y < MB; ++y) am[y] = max(__reduce_max_sync(0xffffffffu, am[y]) >> 7, 15u);
+          for (int y = 0; y < MB; ++y) {
+            am[y] = 0;
 #pragma unroll
-        for (int y = 0; y < MB; ++y) {
-          const int m = m0 + y;
-          if (m >= nt_rows) continue;
-          const float f = __uint_as_float((268u - am[y]) << 23);   // the maximum comes to [2^14, 2^15)
+            for (int i = 0; i < XB / 4; ++i) am[y] = max(am[y], max(v[y][i] & 0x7FFFu, (v[y][i] >> 16) & 0x7FFFu));
+          }
 #pragma unroll
-          for (int i = 0; i < XB / 4; ++i)
-            v[y][i] = pack_f16x2(__uint_as_float(v[y][i] << 16) * f, __uint_as_float(v[y][i] & 0xFFFF0000u) * f);
-          uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
-          if constexpr (XB == 8) *reinterpret_cast<uint2*>(x) = make_uint2(v[y][0], v[y][1]);
-          else *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
-          if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
+          for (int y = 0; y < MB; ++y) am[y] = max(__reduce_max_sync(0xffffffffu, am[y]) >> 7, 15u);
+#pragma unroll
+          for (int y = 0; y < MB; ++y) {
+            const int m = m0 + y;
+            if (MB > 1 && m >= nt_rows) continue;
+            const float f = __uint_as_float((268u - am[y]) << 23);   // the maximum comes to [2^14, 2^15)
+#pragma unroll
+            for (int i = 0; i < XB / 4; ++i)
+              v[y][i] = pack_f16x2(__uint_as_float(v[y][i] << 16) * f, __uint_as_float(v[y][i] & 0xFFFF0000u) * f);
+            uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+            if constexpr (XB == 8) *reinterpret_cast<uint2*>(x) = make_uint2(v[y][0], v[y][1]);
+            else *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
+            if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
+          }
         }
       }
+    };
+    if (P == 4) convert(std::integral_constant<int, 1>{});
+    else convert(std::integral_constant<int, 4>{});
+#pragma unroll 1
+    for (; pre < ST; ++pre) {
+      load_next(pstage);
+      pstage = pstage + 1 == ST ? 0 : pstage + 1;
     }
     __syncthreads();
 
     // ---- the units
-    // B operand: lane (g, t) reads token g of each tile; lanes past the last token repeat it (their
-    // products land in columns that are never stored)
+    // An mma's 16 k-slots are four of each lane t; a lane's slots lie in one scale block, 4 / P lanes to a
+    // block. Column n of a tile is token n / P against block n % P of the step alone: the B operand of
+    // lane (g, t) is zero where its block is not g % P, so that the P blocks' sums stay apart and
+    // one scale each is enough for a whole step. Rows: lane g takes row rg of each octet, the
+    // bit reversal of g, so that neighbours' equal pieces meet different banks.
+    const int rg = (g & 1) << 2 | (g & 2) | g >> 2;
+    const int rsw = CH == 256 ? rg : (rg >> 1) & 3;         // swizzle of the lane's row in each octet
+    const int rd = rg * RB + (((t * LB >> 4) ^ rsw) << 4) + (t * LB & 15), rw = rg * RB + ((t ^ rsw) << 4);   // codes, W_L
     int xa[NT], ba[NT];
+    bool live[NT];
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
-      const int m = min(b * 8 + g, nt_rows - 1);
-      xa[b] = sm.x + m * p.kc * 2 + ((m & 1) << 6) + (V == 32 ? t * 16 : (t >> 1) * 16 + (t & 1) * 8);
-      ba[b] = sm.b + m * sm.bcols * 2 + ((m & 1) << 6) + t * 16;
+      const int m = b * 8 + g / P, mw = min(b * 8 + g, nt_rows - 1);
+      live[b] = m < nt_rows && t / (4 / P) == g % P;
+      // lanes past the last token: zeros, or with P = 1 its repetition (those columns are never stored)
+      const int mx = P == 1 ? mw : m;
+      xa[b] = sm.x + mx * p.kc * 2 + (((mx & 1) << 6) ^ (t * STEP / 2));
+      ba[b] = sm.b + mw * sm.bcols * 2 + ((mw & 1) << 6) + t * 16;
     }
-    const int rsw = CH == 256 ? g : (g >> 1) & 3;           // swizzle of the lane's row in each octet
-    const int rd = g * RB + (rsw << 4) + t * (V == 32 ? 4 : 2), rw = g * RB + ((rsw ^ t) << 4);   // codes, W_L
     auto next_stage = [&] {
       if (++stage == ST) {
         stage = 0;
@@ -459,13 +487,13 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     int off = 0;
     int red = sm.red;                                        // this unit's set of sums (NT = 1)
     for (int u = cta + team * n_cta; u < p.n_units; u += u_step) {
-      float acc[2][NT][4];
+      float acc[2][NT][4], accw[2][NT][4];                  // codes' sums by column; W_L's by token
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.f;
+          for (int i = 0; i < 4; ++i) acc[a][b][i] = accw[a][b][i] = 0.f;
       const int j0 = (twarp - off) & (tw - 1);
       for (int j = j0; j < items; j += tw) {
         // a wait that ran out is recorded: nothing more is loaded, every loop ends, the sums are undefined
@@ -487,8 +515,8 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
               const uint4 x = ld128((ba[b] + (c >> 1) * 128) ^ ((c & 1) * 64));
 #pragma unroll
               for (int a = 0; a < 2; ++a) {
-                mma_bf16(acc[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, x.x, x.y);
-                mma_bf16(acc[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, x.z, x.w);
+                mma_bf16(accw[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, x.x, x.y);
+                mma_bf16(accw[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, x.z, x.w);
               }
             }
           }
@@ -500,67 +528,81 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
             for (int b = 0; b < NT; ++b)
 #pragma unroll
               for (int i = 0; i < 4; ++i) cs[a][b][i] = 0.f;
+          const int ssc = sscale + stage * SBYTES + rg * 16;
 #pragma unroll
           for (int h = 0; h < CH / 128; ++h) {
-            float sc[4][4 * SLOT];                                 // scales of the lane's row in octets 0..3
+            // the scales of the lane's columns 2t, 2t + 1 of each step, for its row in octets 0..3
+            constexpr int STEPS = 128 / STEP, NS = P == 1 ? 1 : 2;
+            float sc[4][STEPS][NS];
 #pragma unroll
             for (int i = 0; i < SLOT; ++i) {
-              const uint4 w = ld128(sscale + stage * SBYTES + (h * SLOT + i) * 128 + g * 16);
-              e8m0x4(w.x, reinterpret_cast<float(&)[4]>(sc[0][4 * i]));
-              e8m0x4(w.y, reinterpret_cast<float(&)[4]>(sc[1][4 * i]));
-              e8m0x4(w.z, reinterpret_cast<float(&)[4]>(sc[2][4 * i]));
-              e8m0x4(w.w, reinterpret_cast<float(&)[4]>(sc[3][4 * i]));
-            }
+              const uint4 w4 = ld128(ssc + (h * SLOT + i) * 128);
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-              uint32_t xb[NT][4];
-#pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                const int x = ((xa[b] + j * (CH * 2)) ^ (blk * 64)) + h * 256;
-                if constexpr (V == 32) {
-                  const uint4 v = ld128(x);
-                  xb[b][0] = v.x; xb[b][1] = v.y; xb[b][2] = v.z; xb[b][3] = v.w;
+              for (int q = 0; q < 4; ++q) {
+                if constexpr (P == 4) {
+                  e8m0x2(w[q] >> ((t & 1) * 16), sc[q][i][0], sc[q][i][NS - 1]);
+                } else if constexpr (P == 2) {
+                  e8m0x2(w[q], sc[q][2 * i][0], sc[q][2 * i][NS - 1]);
+                  e8m0x2(w[q] >> 16, sc[q][2 * i + 1][0], sc[q][2 * i + 1][NS - 1]);
                 } else {
-                  const uint2 u2 = ld64(x), v = ld64(x + 32);
-                  xb[b][0] = u2.x; xb[b][1] = u2.y; xb[b][2] = v.x; xb[b][3] = v.y;
+                  e8m0x2(w[q], sc[q][4 * i][0], sc[q][4 * i + 1][0]);
+                  e8m0x2(w[q] >> 16, sc[q][4 * i + 2][0], sc[q][4 * i + 3][0]);
                 }
               }
-              const int w = (sw + rd) ^ ((h * 4 + blk) * 16);
+            }
+            constexpr int PAIR = LB == 2 ? 2 : 1, LN = STEP / 8 * PAIR;
+            uint32_t fl[2][LN], fh[2][LN];                         // f16 pairs of rows rg and rg + octet, by tile
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st) {
+              constexpr int XN = STEP / 8;                         // a lane's words of a step: tokens
+              constexpr int CO = STEP / 2;                         // a row's code bytes of a step
+              uint32_t xb[NT][XN];
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                // the lane's STEP / 4 channels: 64-byte pieces in the swizzle of odd tokens
+                const int x = xa[b] + j * (CH * 2) + h * 256;
+                constexpr int XO = STEP * 2;
+#pragma unroll
+                for (int i = 0; i < XN; i += 4) {
+                  const int at = P == 1 || live[b] ? (x ^ (st * XO & 255)) + i * 4 : sm.zero + i * 4;
+                  if constexpr (XN >= 4) {
+                    const uint4 v = ld128(at);
+                    xb[b][i] = v.x; xb[b][i + 1] = v.y; xb[b][i + 2] = v.z; xb[b][i + 3] = v.w;
+                  } else {
+                    const uint2 v = ld64(at);
+                    xb[b][0] = v.x; xb[b][1] = v.y;
+                  }
+                }
+              }
+              const int w0b = (sw + rd) ^ (h * 64 + st * CO);
 #pragma unroll
               for (int a = 0; a < 2; ++a) {
-                const int lo = w + a * 16 * RB, hi = lo + 8 * RB;
-                uint32_t wl, wh;
-                if constexpr (V == 32) {
-                  wl = ld32(lo);
-                  wh = ld32(hi);
-                } else {
-                  wl = ld16(lo) | (ld16(lo + 8) << 16);
-                  wh = ld16(hi) | (ld16(hi + 8) << 16);
+                if (st % PAIR == 0) {
+                  load_codes<LB>(smem + w0b + a * 16 * RB, fl[a]);
+                  load_codes<LB>(smem + w0b + (a * 16 + 8) * RB, fh[a]);
                 }
-                uint32_t fl[4], fh[4];
-                e2m1x8_to_f16(wl, fl);
-                e2m1x8_to_f16(wh, fh);
+                const uint32_t* const l = fl[a] + st % PAIR * 2, *const u = fh[a] + st % PAIR * 2;
+                const float s0 = sc[2 * a][st][0], s1 = sc[2 * a][st][NS - 1];
+                const float s2 = sc[2 * a + 1][st][0], s3 = sc[2 * a + 1][st][NS - 1];
 #pragma unroll
-                for (int y = 0; y < SLOT; ++y) {
-                  const float s0 = sc[2 * a][blk * SLOT + y], s1 = sc[2 * a + 1][blk * SLOT + y];
+                for (int b = 0; b < NT; ++b) {
+                  float d[4];
+                  mma_f16_first(d, l[0], u[0], l[1], u[1], xb[b][0], xb[b][1]);
 #pragma unroll
-                  for (int b = 0; b < NT; ++b) {
-                    float d[4];
-                    mma_f16_first(d, fl[2 * y], fh[2 * y], fl[2 * y + 1], fh[2 * y + 1], xb[b][2 * y], xb[b][2 * y + 1]);
-                    if constexpr (V == 32) mma_f16(d, fl[2], fh[2], fl[3], fh[3], xb[b][2], xb[b][3]);
-                    cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
-                    cs[a][b][1] = fmaf(d[1], s0, cs[a][b][1]);
-                    cs[a][b][2] = fmaf(d[2], s1, cs[a][b][2]);
-                    cs[a][b][3] = fmaf(d[3], s1, cs[a][b][3]);
-                  }
+                  for (int i = 2; i < STEP / 8; i += 2) mma_f16(d, l[i], u[i], l[i + 1], u[i + 1], xb[b][i], xb[b][i + 1]);
+                  cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
+                  cs[a][b][1] = fmaf(d[1], s1, cs[a][b][1]);
+                  cs[a][b][2] = fmaf(d[2], s2, cs[a][b][2]);
+                  cs[a][b][3] = fmaf(d[3], s3, cs[a][b][3]);
                 }
               }
             }
           }
 #pragma unroll
           for (int b = 0; b < NT; ++b) {
-            const uint2 f = ld64(sm.xs + (j * 8 * NT + b * 8 + 2 * t) * 4);
-            const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y);
+            const int f = sm.xs + (j * 8 * NT + b * 8 + 2 * t / P) * 4;
+            const float f0 = __uint_as_float(ld32(f)), f1 = P == 1 ? __uint_as_float(ld32(f + 4)) : f0;
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
               acc[a][b][0] = fmaf(cs[a][b][0], f0, acc[a][b][0]);
@@ -586,13 +628,30 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         to = swarp + stage * sm.stage;
         if (lane == 0) at[warp] = to;
       }
+      // the blocks' columns of a token add up to its sum, which then takes its place among the tokens' columns
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            float v0 = acc[a][b][i], v1 = acc[a][b][i + 1];
+            if constexpr (P > 1) {
+              v0 += v1;                                      // P = 2: lane t has token t
+              if constexpr (P == 4) v0 += __shfl_xor_sync(0xffffffffu, v0, 1);   // lanes 2m, 2m + 1 have token m
+              v1 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 2 : min(2 * t + 1, 3)));
+              v0 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 0 : min(2 * t, 3)));
+            }
+            acc[a][b][i] = v0 + accw[a][b][i];
+            acc[a][b][i + 1] = v1 + accw[a][b][i + 1];
+          }
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int m = b * 8 + 2 * t + i;
           if (m >= nt_rows) continue;
-          float* const x = reinterpret_cast<float*>(smem + to) + m * GV_PITCH + g;
+          float* const x = reinterpret_cast<float*>(smem + to) + m * GV_PITCH + rg;
           x[0] = acc[0][b][i];
           x[8] = acc[0][b][2 + i];
           x[16] = acc[1][b][i];
@@ -678,11 +737,11 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int V, int CH, in
 
 constexpr int GV_SMEM_MAX = 232448 - 8192;                   // 227 KB less the static part and a reserve
 
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+template <int V, int CH, int P, int NT, int NW, int ST, bool GROUPED>
 cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, int slots, int n_cta, cudaStream_t s) {
   static PerDeviceOnce attr_once;
   const cudaError_t ae = attr_once.run([] {
-    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(gemv_kernel<V, CH, P, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GV_SMEM_MAX);
   });
   if (ae != cudaSuccess) return ae;
@@ -700,11 +759,11 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, int sl
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED>, maps, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, P, NT, NW, ST, GROUPED>, maps, p);
 }
 
 // The split of one call. CH, NT, NW and ST are the kernel's, mt the tokens of a pass.
-template <int CH, int NT, int NW, int ST, bool GROUPED>
+template <int CH, int P, int NT, int NW, int ST, bool GROUPED>
 cudaError_t launch_v(GemvParams p, int slots, int num_sms, cudaStream_t s) {
   static const int tw_min = getenv("TWM") ? atoi(getenv("TWM")) : 4, tw_units = getenv("TWU") ? atoi(getenv("TWU")) : 2;
   const int V = p.G == 16 ? 16 : 32;
@@ -744,8 +803,8 @@ cudaError_t launch_v(GemvParams p, int slots, int num_sms, cudaStream_t s) {
   }
   n_cta = std::min(n_cta, (p.n_units + teams - 1) / teams);
   p.n_cta = n_cta;
-  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s)
-                 : launch_t<32, CH, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s);
+  return V == 16 ? launch_t<16, CH, P, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s)
+                 : launch_t<32, CH, P, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s);
 }
 
 }  // namespace
@@ -757,19 +816,31 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   p.rows32 = p.N % 32 == 0;
   if (p.expert) {
     const int slots = std::min(p.M, p.E);
-    if (p.M <= 64) {
+    if (p.M <= 16) {
+      p.mt = std::min(p.M, 2);
+      return launch_v<256, 4, 1, 8, 2, true>(p, slots, num_sms, s);
+    }
+    if (p.M <= 128) {
       p.mt = std::min(p.M, 8);
-      return launch_v<256, 1, 8, 2, true>(p, slots, num_sms, s);
+      return launch_v<256, 1, 1, 8, 2, true>(p, slots, num_sms, s);
     }
     p.mt = 16;
-    return launch_v<256, 2, 8, 2, true>(p, slots, num_sms, s);
+    return launch_v<256, 1, 2, 8, 2, true>(p, slots, num_sms, s);
+  }
+  if (p.M <= 2) {
+    p.mt = p.M;
+    return launch_v<256, 4, 1, 16, 2, false>(p, 1, num_sms, s);
+  }
+  if (p.M <= 4) {
+    p.mt = p.M;
+    return launch_v<256, 2, 1, 16, 2, false>(p, 1, num_sms, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    return launch_v<256, 1, 16, 2, false>(p, 1, num_sms, s);
+    return launch_v<256, 1, 1, 8, 3, false>(p, 1, num_sms, s);
   }
   p.mt = std::min(p.M, 16);
-  return launch_v<256, 2, 8, 2, false>(p, 1, num_sms, s);
+  return launch_v<256, 1, 2, 8, 2, false>(p, 1, num_sms, s);
 }
 
 }  // namespace osc
