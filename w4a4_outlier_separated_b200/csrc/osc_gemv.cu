@@ -5,12 +5,14 @@
 //
 // Unit: 32 weight rows, the four octets {q*32 + j*8 .. +7} (q = 0..3) of a 128-row block, because
 // the scale layout keeps exactly those rows' words together: 128 contiguous bytes per 512-byte
-// atom. Item: a unit's codes and scales of 128 channels, or its W_L of 32 columns (both 64 bytes a
-// row). A CTA stages the tokens once, then runs over its units; a team of its warps shares a unit's
-// items. Each warp copies its items into its own ring of stages with cp.async, running ahead over
-// the ends of units, and computes without waiting for another warp. A unit's sums meet in the
-// stages just consumed, in a fixed order. Where one CTA cannot hold the tokens, or the units are
-// fewer than the SMs, a cluster of S CTAs splits K and adds its sums through distributed shared memory.
+// atom. Item: a unit's codes and scales of CH channels, or its W_L of CH / 4 columns (both CH / 2
+// bytes a row). The work is the units of every pass (an expert's rows, mt at a time; the dense form
+// is one expert), in one line; each CTA takes an equal run of it, whose parts of one pass are its
+// segments. A segment stages its tokens once; teams of warps share its units, a team's warps a
+// unit's items. Each warp copies its items by TMA into its own ring of stages, running ahead over the
+// ends of units, and computes without waiting for another warp; a unit's sums meet in shared memory
+// in a fixed order. Where units are few, or one CTA cannot hold the tokens, a cluster of S CTAs
+// splits K and adds its sums through distributed shared memory.
 //
 // Arithmetic: mma.m16n8k16 on f16 operands with fp32 accumulators, the weight rows as the
 // 16-row side and the tokens as the 8-wide side. E2M1 codes become f16 exactly (one conversion
@@ -22,7 +24,6 @@
 // The protected channels are zeroed in the staged tokens and kept apart in bf16; their products
 // with W_L run as bf16 mma into the same sums.
 #include <cuda_fp16.h>
-#include <cstdlib>
 #include <type_traits>
 
 #include "osc_device.cuh"
@@ -40,9 +41,9 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-__device__ __forceinline__ float lds32f_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+__device__ __forceinline__ float4 lds128f_cluster(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
 
@@ -112,6 +113,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// max(|a|, |b|) per bf16 half; the sign bits of the result are junk.
+__device__ __forceinline__ uint32_t maxabs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Rows lr .. lr + 3 of unit u (in one octet), row r of Y.
+__device__ __forceinline__ void store4(const GemvParams& p, int r, int u, int lr, const float4& v) {
+  const int n = (u >> 2) * 128 + (u & 3) * 8 + (lr >> 3) * 32 + (lr & 7);
+  if (n >= p.N) return;
+  const size_t o = (size_t)r * p.N + n;
+  *reinterpret_cast<uint2*>(p.Y + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  if (p.Yf32) *reinterpret_cast<float4*>(p.Yf32 + o) = v;
+}
+
 __device__ __forceinline__ int cluster_id() {
   uint32_t r;
   asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
@@ -121,12 +138,11 @@ __device__ __forceinline__ int cluster_id() {
 // Shared memory of a CTA, in bytes from its start. CH: channels of an item; kc: channels of this
 // CTA's K range (at most); cols: W_L columns.
 struct GvSmem {
-  int stage, warp, sc, x, zero, red, xs, b, bcols, ent, ids, flag, at, total;
+  int stage, warp, sc, x, zero, red, xs, b, bcols, ent, ids, cnt, at, total;
 };
-// A warp's sums, [token][row]: the row pitch of 36 floats keeps the mma fragments' stores (tokens 2t,
-// rows g) and the reads (32 rows) off each other's banks.
-constexpr int GV_PITCH = 36;
-__host__ __device__ constexpr int gv_sums(int NT) { return 8 * NT * GV_PITCH * 4; }
+// A warp's sums: row r of token m at m * 32 + (r ^ (m / 2 % 4) * 8), so that the mma fragments' stores
+// (tokens 2t, rows g) and the reads (4 rows a lane) meet different banks.
+__host__ __device__ constexpr int gv_sums(int NT) { return 8 * NT * GV_ROWS * 4; }
 __host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST, int mt, int kc, int cols, int n_table,
                                           int rows, int E) {
   GvSmem m;
@@ -135,14 +151,14 @@ __host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST,
   m.sc = NW * m.warp;                                              // the stages' scales
   m.x = m.sc + NW * ST * GV_ROWS * CH / V;                         // tokens in f16
   m.zero = m.x + mt * kc * 2;                                      // 64 bytes of zeros
-  m.red = m.zero + 64;                                       // two sets of the warps' sums (NT = 1)
+  m.red = m.zero + 64;                                             // two sets of the warps' sums (NT = 1)
   m.xs = m.red + (NT == 1 ? 2 * NW * gv_sums(NT) : 0);             // the tokens' powers of two, per item
   m.b = (m.xs + kc / CH * NT * 32 + 127) / 128 * 128;              // protected channels' values
   m.bcols = ((cols < n_table ? cols : n_table) + 63) / 64 * 64;
   m.ent = m.b + mt * m.bcols * 2;                                  // table entries with their columns
   m.ids = m.ent + (n_table + 3) / 4 * 16;                          // grouped: expert ids
-  m.flag = m.ids + (rows + 3) / 4 * 16;                            // grouped: experts with rows
-  m.at = m.flag + (E + 3) / 4 * 16;                                // stage that holds a warp's sums (NT = 2)
+  m.cnt = m.ids + (rows + 3) / 4 * 16;                             // grouped: rows of each expert
+  m.at = m.cnt + (E + 3) / 4 * 16;                                 // where a warp's sums lie (NT = 2)
   m.total = m.at + NW * 4 + 1024;                                  // and room to start at a multiple of 1024
   return m;
 }
@@ -155,36 +171,33 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 }  // namespace
 
-// V: channels of a scale slot; CH: channels of an item; P: scale blocks of an mma; NT: token tiles of 8; NW: warps; ST: stages
-// per warp.
-template <int V, int CH, int P, int NT, int NW, int ST, bool GROUPED>
+// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp.
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
 __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ uint64_t s_full[NW][ST];   // a stage's data has arrived
   __shared__ int s_abort;
   __shared__ int s_scan[2][NW];
-  __shared__ int s_cols[2];   // first W_L column of this CTA's K range, one past the last
-  __shared__ int s_list[16];  // this pass's rows of Y (grouped)
-  __shared__ int s_slot[3];   // rows of this pass, where the next one starts, the expert
-  __shared__ float s_sum[GV_ROWS * 8 * NT];
+  __shared__ int s_cols[2];             // first W_L column of this CTA's K range, one past the last
+  __shared__ int s_list[16];            // the segment's rows of Y (grouped)
+  __shared__ int s_seg[5];              // the segment's expert, first row of its pass, rows, first unit; all work
+  __shared__ __align__(16) float s_sum[GV_ROWS * 8 * NT];
   constexpr int THREADS = NW * 32;
   constexpr int SLOT = 32 / V;                             // scale slots of 32 channels
-  constexpr int STEP = V * P;                              // channels of a step: P scale blocks
-  constexpr int LB = STEP / 8;                             // a lane's code bytes of a step and row
   constexpr int RB = CH / 2;                               // bytes of an item's row: codes, or CH / 4 W_L columns
   constexpr int COLS = CH / 4;
   constexpr int SBYTES = GV_ROWS * CH / V;                 // scales of an item
+  constexpr int XB = CH / 16;                              // bytes of a lane when an item's tokens are copied
   static_assert(NT == 1 || gv_sums(NT) <= GV_ROWS * RB, "a stage takes a warp's sums");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S;
-  const int cta = S == 1 ? blockIdx.x : cluster_id(), rank = S == 1 ? 0 : cluster_ctarank(), n_cta = p.n_cta;
+  const int cta = S == 1 ? blockIdx.x : cluster_id(), rank = S == 1 ? 0 : cluster_ctarank();
   const int N = p.N, K = p.K;
   const int n_table = p.L ? (K >> p.g_shift) * p.R : 0;
   const GvSmem sm = gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
   const uint32_t sbase = smem_u32(smem);
   const int swarp = warp * sm.warp, sscale = sm.sc + warp * (ST * SBYTES);
-  const int tw = 1 << p.tw_shift, team = warp >> p.tw_shift, twarp = warp & (tw - 1);
   auto ld32 = [&](int off) { return *reinterpret_cast<const uint32_t*>(smem + off); };
   auto ld64 = [&](int off) { return *reinterpret_cast<const uint2*>(smem + off); };
   auto ld128 = [&](int off) { return *reinterpret_cast<const uint4*>(smem + off); };
@@ -209,106 +222,133 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- which expert (grouped)
-  int e = 0;
+  // ---- the rows of each expert (grouped)
   int* const ids = reinterpret_cast<int*>(smem + sm.ids);
+  int* const cnt = reinterpret_cast<int*>(smem + sm.cnt);
   if constexpr (GROUPED) {
-    int* const flag = reinterpret_cast<int*>(smem + sm.flag);
-    for (int i = tid; i < p.E; i += THREADS) flag[i] = 0;
+    for (int i = tid; i < p.E; i += THREADS) cnt[i] = 0;
     __syncthreads();
     for (int r = tid; r < p.M; r += THREADS) {
       const int id = p.expert[r];
       ids[r] = id;
-      if (id >= 0 && id < p.E) flag[id] = 1;
-      else if (id >= p.E && blockIdx.x == 0 && blockIdx.y == 0) record_status(p.status, DEV_BAD_TABLE);
+      if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
+      else if (id >= p.E && cta == 0) record_status(p.status, DEV_BAD_TABLE);
     }
     __syncthreads();
-    if (blockIdx.y == 0) {
-      // rows without an expert come out as zeros
-      for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
-        if (ids[r] >= 0 && ids[r] < p.E) continue;
-        for (int n = tid; n < N; n += THREADS) {
-          p.Y[(size_t)r * N + n] = 0;
-          if (p.Yf32) p.Yf32[(size_t)r * N + n] = 0.f;
-        }
+    // rows without an expert come out as zeros
+    for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
+      if (ids[r] >= 0 && ids[r] < p.E) continue;
+      for (int n = tid; n < N; n += THREADS) {
+        p.Y[(size_t)r * N + n] = 0;
+        if (p.Yf32) p.Yf32[(size_t)r * N + n] = 0.f;
       }
     }
     if (warp == 0) {
-      // the blockIdx.y-th expert (ascending) that has rows
-      int left = blockIdx.y, found = -1;
-      for (int b = 0; b < p.E; b += 32) {
-        const unsigned m = __ballot_sync(0xffffffffu, b + lane < p.E && flag[b + lane] != 0);
-        const int c = __popc(m);
-        if (left < c) {
-          found = b + (int)__fns(m, 0, left + 1);
-          break;
-        }
-        left -= c;
-      }
-      if (lane == 0) s_slot[2] = found;
+      int passes = 0;
+      for (int i = lane; i < p.E; i += 32) passes += (cnt[i] + p.mt - 1) / p.mt;
+      passes = __reduce_add_sync(0xffffffffu, passes);
+      if (lane == 0) s_seg[4] = passes * p.n_units;
     }
     __syncthreads();
-    e = s_slot[2];
-    if (e < 0) return;                                   // the same for the whole cluster
   }
-  const int8_t* const L = p.L + (size_t)e * n_table;
-  const int wrow0 = GROUPED ? e * N : 0;                   // the expert's first row of QW and W_L
-  const int sblk0 = GROUPED ? e * ((N + 127) / 128) : 0;   // and 128-row block of SW
+  // this CTA's run of the work
+  const long long total = GROUPED ? s_seg[4] : p.work;
+  long long wa = total * cta / p.n_cta;
+  const long long wb = total * (cta + 1) / p.n_cta;
+
   int stage = 0;                                           // of the next item to use
   uint32_t parity = 0;                                     // of its barrier
   bool dead = false;                                       // a wait ran out
-
-  for (int tile0 = GROUPED ? 0 : blockIdx.y * p.mt;;) {
-    // ---- this pass's tokens: at most mt rows
-    int nt_rows;
+  while (wa < wb) {
+    // ---- the segment: units u0 .. u1 - 1 of one pass over expert e
+    int e = 0, tile0, nt_rows, u0;
     if constexpr (GROUPED) {
       if (warp == 0) {
-        // the next mt rows of expert e, in ascending order
-        int have = 0, r = tile0;
-        for (; r < p.M && have < p.mt; r += 32) {
-          const bool hit = r + lane < p.M && ids[r + lane] == e;
-          const unsigned m = __ballot_sync(0xffffffffu, hit);
-          const int at = have + __popc(m & ((1u << lane) - 1u));
-          if (hit && at < p.mt) s_list[at] = r + lane;
-          const int c = __popc(m);
-          if (have + c > p.mt) {                          // go on behind the last row taken
-            r += (int)__fns(m, 0, p.mt - have + 1);
-            have = p.mt;
+        // the expert whose passes hold unit wa of the work
+        int at = (int)(wa / p.n_units), b = 0, first = 0;
+        for (;; b += 32) {
+          const int c = b + lane < p.E ? (cnt[b + lane] + p.mt - 1) / p.mt : 0;
+          int sum = c;                                     // inclusive over the lanes
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+          }
+          const unsigned m = __ballot_sync(0xffffffffu, at < sum);
+          if (m) {
+            const int l = __ffs(m) - 1;
+            e = b + l;
+            first = (at - __shfl_sync(0xffffffffu, sum - c, l)) * p.mt;
             break;
           }
-          have += c;
+          at -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        // its rows first .. first + mt - 1, in ascending order
+        int have = -first;
+        for (int r = 0; r < p.M && have < p.mt; r += 32) {
+          const bool hit = r + lane < p.M && ids[r + lane] == e;
+          const unsigned m = __ballot_sync(0xffffffffu, hit);
+          const int i = have + __popc(m & ((1u << lane) - 1u));
+          if (hit && i >= 0 && i < p.mt) s_list[i] = r + lane;
+          have += __popc(m);
         }
         if (lane == 0) {
-          s_slot[0] = have;
-          s_slot[1] = min(r, p.M);
+          s_seg[0] = e;
+          s_seg[2] = min(have, p.mt);
+          s_seg[3] = (int)(wa % p.n_units);
         }
       }
       __syncthreads();
-      nt_rows = s_slot[0];
-      tile0 = s_slot[1];
-      if (nt_rows == 0) break;
+      e = s_seg[0];
+      tile0 = 0;
+      nt_rows = s_seg[2];
+      u0 = s_seg[3];
     } else {
+      const int pass = p.work == p.n_units ? 0 : (int)(wa / p.n_units);
+      tile0 = pass * p.mt;
       nt_rows = min(p.mt, p.M - tile0);
+      u0 = (int)(wa - (long long)pass * p.n_units);
     }
+    const int u1 = (int)min((long long)p.n_units, u0 + (wb - wa));
+    wa += u1 - u0;
+    // teams: as many as four where there are units for them; every warp of a team has items of every unit
+    int tw_shift = 31 - __clz(NW);
+    if (S == 1) {
+      tw_shift -= u1 - u0 >= 4 ? 2 : u1 - u0 >= 2 ? 1 : 0;
+      while ((1 << tw_shift) > nc) --tw_shift;
+    }
+    const int tw = 1 << tw_shift, teams = NW >> tw_shift, team = warp >> tw_shift, twarp = warp & (tw - 1);
+    const int8_t* const L = p.L + (size_t)e * n_table;
+    const int wrow0 = GROUPED ? e * N : 0;                 // the expert's first row of QW and W_L
+    const int sblk0 = GROUPED ? e * ((N + 127) / 128) : 0; // and 128-row block of SW
     auto xrow = [&](int m) -> const uint16_t* {
       if constexpr (GROUPED) return p.X + (size_t)(s_list[m] / p.fan) * K;
       else return p.X + (size_t)(tile0 + m) * K;
     };
 
+    // ---- what the rest waits for first: the table, and the tokens as they are (each warp the items
+    // it will convert)
+    const int8_t l_first = tid < n_table ? L[tid] : -1;
+    for (int c = warp; c < nc; c += NW)
+#pragma unroll 4
+      for (int m = 0; m < nt_rows; ++m)
+        cp_async<XB>(sbase + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6)),
+                     xrow(m) + (size_t)(c0 + c) * CH + lane * (CH / 32));
+
     // ---- start the weight stream: the next item to load is pj of unit pu. Items 0 .. nc - 1 of a
-    // unit are codes; the W_L columns' items follow, known only after the table has been read.
-    const int u_step = n_cta * (NW >> p.tw_shift);
+    // unit are codes; the W_L columns' items follow, known only after the table has been read. The
+    // first item of a unit goes to the next warp of the team in each unit.
     int items = 0x7FFFFFFF, w0 = 0;
-    int pu = dead ? p.n_units : cta + team * n_cta, poff = 0, pj = twarp;
+    int pu = dead ? u1 : u0 + team, poff = 0, pj = twarp;
     auto settle = [&] {                                    // past the end of a unit: to the next one
-      while (pj >= items && pu < p.n_units) {
-        pu += u_step;
+      while (pj >= items && pu < u1) {
+        pu += teams;
         poff += items;
         pj = (twarp - poff) & (tw - 1);
       }
     };
     auto load_next = [&](int to) {
-      if (pu >= p.n_units) return;
+      if (pu >= u1) return;
       if (lane == 0) {
         const uint32_t sw = sbase + swarp + to * sm.stage, bar = bars + to * 8;
         const bool main = pj < nc;
@@ -328,21 +368,12 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       pj += tw;
       if (pj >= items) settle();
     };
-    const int8_t l_first = tid < n_table ? L[tid] : -1;    // on its way before the bulk of the data
-    // the tokens, as they are: each warp copies the items it will convert
-    constexpr int XB = CH / 16;                            // bytes of a lane
-    for (int c = warp; c < nc; c += NW)
-#pragma unroll 4
-      for (int m = 0; m < nt_rows; ++m)
-        cp_async<XB>(sbase + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6)),
-                     xrow(m) + (size_t)(c0 + c) * CH + lane * (CH / 32));
-
-    int pre = 0;
-    int pstage = stage;
-#pragma unroll 1
-    for (; pre < 1 && pj < nc; ++pre) {       // one item; the others when the tokens are staged
+    // one item now, the others when the tokens are staged, so that these do not queue behind them
+    int pre = 0, pstage = stage;
+    if (pj < nc) {
       load_next(pstage);
       pstage = pstage + 1 == ST ? 0 : pstage + 1;
+      pre = 1;
     }
 
     // ---- the table: each entry with its W_L column (-1: none)
@@ -356,7 +387,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         const int i = b + tid;
         int v = b == 0 ? (int)l_first : i < n_table ? (int)L[i] : -1;
         if (v >= p.G) {
-          if (blockIdx.x == 0) record_status(p.status, DEV_BAD_TABLE);
+          if (u0 == 0) record_status(p.status, DEV_BAD_TABLE);
           v = -1;
         }
         const unsigned m = __ballot_sync(0xffffffffu, v >= 0);
@@ -368,7 +399,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         if (i == e0) s_cols[0] = col;
         if (i == e1) s_cols[1] = col;
         if (v >= 0 && col >= p.K_L) {
-          if (blockIdx.x == 0) record_status(p.status, DEV_BAD_TABLE);
+          if (u0 == 0) record_status(p.status, DEV_BAD_TABLE);
           v = -1;
         }
         if (i < n_table) ent[i] = v >= 0 ? col << 8 | v : -1;
@@ -386,16 +417,17 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     // different banks)
     cp_async_wait_all();
     auto convert = [&](auto mb) {
-      constexpr int MB = decltype(mb)::value;                // tokens at a time, for their latencies' sake
+      constexpr int MB = decltype(mb)::value;              // tokens at a time, for their latencies' sake
       for (int c = warp; c < nc; c += NW) {
         const int k = (c0 + c) * CH + lane * (CH / 32);
         const int grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
+        uint8_t* const xc = smem + sm.x + c * CH * 2;
         for (int m0 = 0; m0 < nt_rows; m0 += MB) {
           uint32_t v[MB][XB / 4], am[MB];
 #pragma unroll
           for (int y = 0; y < MB; ++y) {
             const int m = MB == 1 ? m0 : min(m0 + y, nt_rows - 1);
-            const uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+            const uint8_t* const x = xc + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6));
             if constexpr (XB == 8) {
               const uint2 q = *reinterpret_cast<const uint2*>(x);
               v[y][0] = q.x; v[y][1] = q.y;
@@ -427,9 +459,9 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           __syncwarp();
 #pragma unroll
           for (int y = 0; y < MB; ++y) {
-            am[y] = 0;
-#pragma unroll
-            for (int i = 0; i < XB / 4; ++i) am[y] = max(am[y], max(v[y][i] & 0x7FFFu, (v[y][i] >> 16) & 0x7FFFu));
+            uint32_t a = maxabs2(v[y][0], v[y][1]);
+            if constexpr (XB == 16) a = maxabs2(a, maxabs2(v[y][2], v[y][3]));
+            am[y] = max(a & 0x7FFFu, (a >> 16) & 0x7FFFu);
           }
 #pragma unroll
           for (int y = 0; y < MB; ++y) am[y] = max(__reduce_max_sync(0xffffffffu, am[y]) >> 7, 15u);
@@ -441,7 +473,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < XB / 4; ++i)
               v[y][i] = pack_f16x2(__uint_as_float(v[y][i] << 16) * f, __uint_as_float(v[y][i] & 0xFFFF0000u) * f);
-            uint8_t* const x = smem + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6));
+            uint8_t* const x = xc + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6));
             if constexpr (XB == 8) *reinterpret_cast<uint2*>(x) = make_uint2(v[y][0], v[y][1]);
             else *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
             if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
@@ -449,7 +481,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         }
       }
     };
-    if (P == 4) convert(std::integral_constant<int, 1>{});
+    if (nt_rows <= 2) convert(std::integral_constant<int, 1>{});
     else convert(std::integral_constant<int, 4>{});
 #pragma unroll 1
     for (; pre < ST; ++pre) {
@@ -458,250 +490,262 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     }
     __syncthreads();
 
-    // ---- the units
-    // An mma's 16 k-slots are four of each lane t; a lane's slots lie in one scale block, 4 / P lanes to a
-    // block. Column n of a tile is token n / P against block n % P of the step alone: the B operand of
-    // lane (g, t) is zero where its block is not g % P, so that the P blocks' sums stay apart and
-    // one scale each is enough for a whole step. Rows: lane g takes row rg of each octet, the
-    // bit reversal of g, so that neighbours' equal pieces meet different banks.
-    const int rg = (g & 1) << 2 | (g & 2) | g >> 2;
-    const int rsw = CH == 256 ? rg : (rg >> 1) & 3;         // swizzle of the lane's row in each octet
-    const int rd = rg * RB + (((t * LB >> 4) ^ rsw) << 4) + (t * LB & 15), rw = rg * RB + ((t ^ rsw) << 4);   // codes, W_L
-    int xa[NT], ba[NT];
-    bool live[NT];
+    // ---- the units. P: scale blocks of an mma. An mma's 16 k-slots are four of each lane t; a lane's slots
+    // lie in one scale block, 4 / P lanes to a block. Column n of a tile is token n / P against block n % P
+    // of the step alone: the B operand of lane (g, t) is zero where its block is not g % P, so that the P
+    // blocks' sums stay apart and one scale each is enough for a step of P blocks. Rows: lane g takes
+    // row rg of each octet, the bit reversal of g, so that neighbours' equal pieces meet different banks.
+    auto run = [&](auto pc) {
+      constexpr int P = decltype(pc)::value;
+      constexpr int STEP = V * P;                          // channels of a step
+      constexpr int LB = STEP / 8;                         // a lane's code bytes of a step and row
+      const int rg = (g & 1) << 2 | (g & 2) | g >> 2;
+      const int rsw = CH == 256 ? rg : (rg >> 1) & 3;      // swizzle of the lane's row in each octet
+      const int rd = rg * RB + (((t * LB >> 4) ^ rsw) << 4) + (t * LB & 15), rw = rg * RB + ((t ^ rsw) << 4);   // codes, W_L
+      int xa[NT], ba[NT];
+      bool live[NT];
 #pragma unroll
-    for (int b = 0; b < NT; ++b) {
-      const int m = b * 8 + g / P, mw = min(b * 8 + g, nt_rows - 1);
-      live[b] = m < nt_rows && t / (4 / P) == g % P;
-      // lanes past the last token: zeros, or with P = 1 its repetition (those columns are never stored)
-      const int mx = P == 1 ? mw : m;
-      xa[b] = sm.x + mx * p.kc * 2 + (((mx & 1) << 6) ^ (t * STEP / 2));
-      ba[b] = sm.b + mw * sm.bcols * 2 + ((mw & 1) << 6) + t * 16;
-    }
-    auto next_stage = [&] {
-      if (++stage == ST) {
-        stage = 0;
-        parity ^= 1;
+      for (int b = 0; b < NT; ++b) {
+        const int m = b * 8 + g / P, mw = min(b * 8 + g, nt_rows - 1);
+        live[b] = m < nt_rows && t / (4 / P) == g % P;
+        // lanes past the last token: zeros, or with P = 1 its repetition (those columns are never stored)
+        const int mx = P == 1 ? mw : m;
+        xa[b] = sm.x + mx * p.kc * 2 + (((mx & 1) << 6) ^ (t * STEP / 2));
+        ba[b] = sm.b + mw * sm.bcols * 2 + ((mw & 1) << 6) + t * 16;
       }
-    };
-    int off = 0;
-    int red = sm.red;                                        // this unit's set of sums (NT = 1)
-    for (int u = cta + team * n_cta; u < p.n_units; u += u_step) {
-      float acc[2][NT][4], accw[2][NT][4];                  // codes' sums by column; W_L's by token
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[a][b][i] = accw[a][b][i] = 0.f;
-      const int j0 = (twarp - off) & (tw - 1);
-      for (int j = j0; j < items; j += tw) {
-        // a wait that ran out is recorded: nothing more is loaded, every loop ends, the sums are undefined
-        if (!mbar_wait(bars + stage * 8, parity, &s_abort, p.status)) {
-          dead = true;
-          pu = p.n_units;
+      auto next_stage = [&] {
+        if (++stage == ST) {
+          stage = 0;
+          parity ^= 1;
         }
-        const int sw = swarp + stage * sm.stage;
-        if (j >= nc) {
-          // protected channels: COLS columns of W_L
-#pragma unroll
-          for (int h = 0; h < CH / 128; ++h) {
-            uint4 wl[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) wl[q] = ld128(((sw + rw) ^ (h * 64)) + q * 8 * RB);
-#pragma unroll
-            for (int b = 0; b < NT; ++b) {
-              const int c = (w0 + j - nc) * (COLS / 32) + h;
-              const uint4 x = ld128((ba[b] + (c >> 1) * 128) ^ ((c & 1) * 64));
-#pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                mma_bf16(accw[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, x.x, x.y);
-                mma_bf16(accw[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, x.z, x.w);
-              }
-            }
-          }
-        } else {
-          float cs[2][NT][4];
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) cs[a][b][i] = 0.f;
-          const int ssc = sscale + stage * SBYTES + rg * 16;
-#pragma unroll
-          for (int h = 0; h < CH / 128; ++h) {
-            // the scales of the lane's columns 2t, 2t + 1 of each step, for its row in octets 0..3
-            constexpr int STEPS = 128 / STEP, NS = P == 1 ? 1 : 2;
-            float sc[4][STEPS][NS];
-#pragma unroll
-            for (int i = 0; i < SLOT; ++i) {
-              const uint4 w4 = ld128(ssc + (h * SLOT + i) * 128);
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if constexpr (P == 4) {
-                  e8m0x2(w[q] >> ((t & 1) * 16), sc[q][i][0], sc[q][i][NS - 1]);
-                } else if constexpr (P == 2) {
-                  e8m0x2(w[q], sc[q][2 * i][0], sc[q][2 * i][NS - 1]);
-                  e8m0x2(w[q] >> 16, sc[q][2 * i + 1][0], sc[q][2 * i + 1][NS - 1]);
-                } else {
-                  e8m0x2(w[q], sc[q][4 * i][0], sc[q][4 * i + 1][0]);
-                  e8m0x2(w[q] >> 16, sc[q][4 * i + 2][0], sc[q][4 * i + 3][0]);
-                }
-              }
-            }
-            constexpr int PAIR = LB == 2 ? 2 : 1, LN = STEP / 8 * PAIR;
-            uint32_t fl[2][LN], fh[2][LN];                         // f16 pairs of rows rg and rg + octet, by tile
-#pragma unroll
-            for (int st = 0; st < STEPS; ++st) {
-              constexpr int XN = STEP / 8;                         // a lane's words of a step: tokens
-              constexpr int CO = STEP / 2;                         // a row's code bytes of a step
-              uint32_t xb[NT][XN];
-#pragma unroll
-              for (int b = 0; b < NT; ++b) {
-                // the lane's STEP / 4 channels: 64-byte pieces in the swizzle of odd tokens
-                const int x = xa[b] + j * (CH * 2) + h * 256;
-                constexpr int XO = STEP * 2;
-#pragma unroll
-                for (int i = 0; i < XN; i += 4) {
-                  const int at = P == 1 || live[b] ? (x ^ (st * XO & 255)) + i * 4 : sm.zero + i * 4;
-                  if constexpr (XN >= 4) {
-                    const uint4 v = ld128(at);
-                    xb[b][i] = v.x; xb[b][i + 1] = v.y; xb[b][i + 2] = v.z; xb[b][i + 3] = v.w;
-                  } else {
-                    const uint2 v = ld64(at);
-                    xb[b][0] = v.x; xb[b][1] = v.y;
-                  }
-                }
-              }
-              const int w0b = (sw + rd) ^ (h * 64 + st * CO);
-#pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                if (st % PAIR == 0) {
-                  load_codes<LB>(smem + w0b + a * 16 * RB, fl[a]);
-                  load_codes<LB>(smem + w0b + (a * 16 + 8) * RB, fh[a]);
-                }
-                const uint32_t* const l = fl[a] + st % PAIR * 2, *const u = fh[a] + st % PAIR * 2;
-                const float s0 = sc[2 * a][st][0], s1 = sc[2 * a][st][NS - 1];
-                const float s2 = sc[2 * a + 1][st][0], s3 = sc[2 * a + 1][st][NS - 1];
-#pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                  float d[4];
-                  mma_f16_first(d, l[0], u[0], l[1], u[1], xb[b][0], xb[b][1]);
-#pragma unroll
-                  for (int i = 2; i < STEP / 8; i += 2) mma_f16(d, l[i], u[i], l[i + 1], u[i + 1], xb[b][i], xb[b][i + 1]);
-                  cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
-                  cs[a][b][1] = fmaf(d[1], s1, cs[a][b][1]);
-                  cs[a][b][2] = fmaf(d[2], s2, cs[a][b][2]);
-                  cs[a][b][3] = fmaf(d[3], s3, cs[a][b][3]);
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int b = 0; b < NT; ++b) {
-            const int f = sm.xs + (j * 8 * NT + b * 8 + 2 * t / P) * 4;
-            const float f0 = __uint_as_float(ld32(f)), f1 = P == 1 ? __uint_as_float(ld32(f + 4)) : f0;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              acc[a][b][0] = fmaf(cs[a][b][0], f0, acc[a][b][0]);
-              acc[a][b][1] = fmaf(cs[a][b][1], f1, acc[a][b][1]);
-              acc[a][b][2] = fmaf(cs[a][b][2], f0, acc[a][b][2]);
-              acc[a][b][3] = fmaf(cs[a][b][3], f1, acc[a][b][3]);
-            }
-          }
-        }
-        if (NT == 1 || j + tw < items) {                     // NT = 2: the last stage takes the sums first
-          __syncwarp();
-          load_next(stage);
-          next_stage();
-        }
-      }
-
-      // ---- join the team's sums (every warp has had an item): in one of two sets (the other may still
-      // be being read), or where these do not fit (NT = 2) in the stage just consumed
-      int* const at = reinterpret_cast<int*>(smem + sm.at);
-      int to = red + warp * gv_sums(NT);
-      if constexpr (NT == 2) {
-        __syncwarp();
-        to = swarp + stage * sm.stage;
-        if (lane == 0) at[warp] = to;
-      }
-      // the blocks' columns of a token add up to its sum, which then takes its place among the tokens' columns
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
+      };
+      int off = 0;
+      int red = sm.red;                                    // this unit's set of sums (NT = 1)
+      for (int u = u0 + team; u < u1; u += teams) {
+        float acc[2][NT][4], accw[2][NT][4];               // codes' sums by column; W_L's by token
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            float v0 = acc[a][b][i], v1 = acc[a][b][i + 1];
-            if constexpr (P > 1) {
-              v0 += v1;                                      // P = 2: lane t has token t
-              if constexpr (P == 4) v0 += __shfl_xor_sync(0xffffffffu, v0, 1);   // lanes 2m, 2m + 1 have token m
-              v1 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 2 : min(2 * t + 1, 3)));
-              v0 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 0 : min(2 * t, 3)));
-            }
-            acc[a][b][i] = v0 + accw[a][b][i];
-            acc[a][b][i + 1] = v1 + accw[a][b][i + 1];
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[a][b][i] = accw[a][b][i] = 0.f;
+        const int j0 = (twarp - off) & (tw - 1);
+        for (int j = j0; j < items; j += tw) {
+          // a wait that ran out is recorded: nothing more is loaded, every loop ends, the sums are undefined
+          if (!mbar_wait(bars + stage * 8, parity, &s_abort, p.status)) {
+            dead = true;
+            pu = u1;
           }
+          const int sw = swarp + stage * sm.stage;
+          if (j >= nc) {
+            // protected channels: COLS columns of W_L
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+            for (int h = 0; h < CH / 128; ++h) {
+              uint4 wl[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int m = b * 8 + 2 * t + i;
-          if (m >= nt_rows) continue;
-          float* const x = reinterpret_cast<float*>(smem + to) + m * GV_PITCH + rg;
-          x[0] = acc[0][b][i];
-          x[8] = acc[0][b][2 + i];
-          x[16] = acc[1][b][i];
-          x[24] = acc[1][b][2 + i];
+              for (int q = 0; q < 4; ++q) wl[q] = ld128(((sw + rw) ^ (h * 64)) + q * 8 * RB);
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                const int c = (w0 + j - nc) * (COLS / 32) + h;
+                const uint4 x = ld128((ba[b] + (c >> 1) * 128) ^ ((c & 1) * 64));
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                  mma_bf16(accw[a][b], wl[2 * a].x, wl[2 * a + 1].x, wl[2 * a].y, wl[2 * a + 1].y, x.x, x.y);
+                  mma_bf16(accw[a][b], wl[2 * a].z, wl[2 * a + 1].z, wl[2 * a].w, wl[2 * a + 1].w, x.z, x.w);
+                }
+              }
+            }
+          } else {
+            float cs[2][NT][4];
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[a][b][i] = 0.f;
+            const int ssc = sscale + stage * SBYTES + rg * 16;
+#pragma unroll
+            for (int h = 0; h < CH / 128; ++h) {
+              // the scales of the lane's columns 2t, 2t + 1 of each step, for its row in octets 0..3
+              constexpr int STEPS = 128 / STEP, NS = P == 1 ? 1 : 2;
+              float sc[4][STEPS][NS];
+#pragma unroll
+              for (int i = 0; i < SLOT; ++i) {
+                const uint4 w4 = ld128(ssc + (h * SLOT + i) * 128);
+                const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if constexpr (P == 4) {
+                    e8m0x2(w[q] >> ((t & 1) * 16), sc[q][i][0], sc[q][i][NS - 1]);
+                  } else if constexpr (P == 2) {
+                    e8m0x2(w[q], sc[q][2 * i][0], sc[q][2 * i][NS - 1]);
+                    e8m0x2(w[q] >> 16, sc[q][2 * i + 1][0], sc[q][2 * i + 1][NS - 1]);
+                  } else {
+                    e8m0x2(w[q], sc[q][4 * i][0], sc[q][4 * i + 1][0]);
+                    e8m0x2(w[q] >> 16, sc[q][4 * i + 2][0], sc[q][4 * i + 3][0]);
+                  }
+                }
+              }
+              constexpr int PAIR = LB == 2 ? 2 : 1, LN = STEP / 8 * PAIR;
+              uint32_t fl[2][LN], fh[2][LN];               // f16 pairs of rows rg and rg + octet, by tile
+#pragma unroll
+              for (int st = 0; st < STEPS; ++st) {
+                constexpr int XN = STEP / 8;               // a lane's words of a step: tokens
+                constexpr int CO = STEP / 2, XO = STEP * 2;   // a row's code bytes, a token's bytes of a step
+                uint32_t xb[NT][XN];
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                  const int x = xa[b] + j * (CH * 2) + h * 256;
+#pragma unroll
+                  for (int i = 0; i < XN; i += 4) {
+                    const int at = P == 1 || live[b] ? (x ^ (st * XO & 255)) + i * 4 : sm.zero + i * 4;
+                    if constexpr (XN >= 4) {
+                      const uint4 v = ld128(at);
+                      xb[b][i] = v.x; xb[b][i + 1] = v.y; xb[b][i + 2] = v.z; xb[b][i + 3] = v.w;
+                    } else {
+                      const uint2 v = ld64(at);
+                      xb[b][0] = v.x; xb[b][1] = v.y;
+                    }
+                  }
+                }
+                const int w0b = (sw + rd) ^ (h * 64 + st * CO);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                  if (st % PAIR == 0) {
+                    load_codes<LB>(smem + w0b + a * 16 * RB, fl[a]);
+                    load_codes<LB>(smem + w0b + (a * 16 + 8) * RB, fh[a]);
+                  }
+                  const uint32_t* const l = fl[a] + st % PAIR * 2, *const h8 = fh[a] + st % PAIR * 2;
+                  const float s0 = sc[2 * a][st][0], s1 = sc[2 * a][st][NS - 1];
+                  const float s2 = sc[2 * a + 1][st][0], s3 = sc[2 * a + 1][st][NS - 1];
+#pragma unroll
+                  for (int b = 0; b < NT; ++b) {
+                    float d[4];
+                    mma_f16_first(d, l[0], h8[0], l[1], h8[1], xb[b][0], xb[b][1]);
+#pragma unroll
+                    for (int i = 2; i < STEP / 8; i += 2) mma_f16(d, l[i], h8[i], l[i + 1], h8[i + 1], xb[b][i], xb[b][i + 1]);
+                    cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
+                    cs[a][b][1] = fmaf(d[1], s1, cs[a][b][1]);
+                    cs[a][b][2] = fmaf(d[2], s2, cs[a][b][2]);
+                    cs[a][b][3] = fmaf(d[3], s3, cs[a][b][3]);
+                  }
+                }
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+              const int f = sm.xs + (j * 8 * NT + b * 8 + 2 * t / P) * 4;
+              const float f0 = __uint_as_float(ld32(f)), f1 = P == 1 ? __uint_as_float(ld32(f + 4)) : f0;
+#pragma unroll
+              for (int a = 0; a < 2; ++a) {
+                acc[a][b][0] = fmaf(cs[a][b][0], f0, acc[a][b][0]);
+                acc[a][b][1] = fmaf(cs[a][b][1], f1, acc[a][b][1]);
+                acc[a][b][2] = fmaf(cs[a][b][2], f0, acc[a][b][2]);
+                acc[a][b][3] = fmaf(cs[a][b][3], f1, acc[a][b][3]);
+              }
+            }
+          }
+          if (NT == 1 || j + tw < items) {                 // NT = 2: the last stage takes the sums first
+            __syncwarp();
+            load_next(stage);
+            next_stage();
+          }
         }
-      if (NT == 2) fence_proxy_async_smem();                 // the next copy into this stage comes after
-      team_sync(1 + team, tw * 32);
-      const int row0 = (u >> 2) * 128 + (u & 3) * 8;
-      auto store = [&](int m, int lr, float v) {
-        const int n = row0 + (lr >> 3) * 32 + (lr & 7);
-        if (n >= N) return;
-        size_t r;
-        if constexpr (GROUPED) r = (size_t)s_list[m];
-        else r = (size_t)(tile0 + m);
-        __nv_bfloat16 h = __float2bfloat16_rn(v);
-        p.Y[r * N + n] = *reinterpret_cast<uint16_t*>(&h);
-        if (p.Yf32) p.Yf32[r * N + n] = v;
-      };
-      // a warp sums a token's 32 rows over the team, another warp's turn first in each unit
-      for (int m = j0; m < nt_rows; m += tw) {
-        float v = 0.f;
-#pragma unroll 8
-        for (int w = team * tw; w < team * tw + tw; ++w) {
-          const int from = NT == 1 ? red + w * gv_sums(NT) : at[w];
-          v += reinterpret_cast<const float*>(smem + from)[m * GV_PITCH + lane];
+
+        // ---- join the team's sums (every warp has had an item): in one of two sets (the other may still
+        // be being read), or where these do not fit (NT = 2) in the stage just consumed
+        int* const at = reinterpret_cast<int*>(smem + sm.at);
+        int to = red + warp * gv_sums(NT);
+        if constexpr (NT == 2) {
+          __syncwarp();
+          to = swarp + stage * sm.stage;
+          if (lane == 0) at[warp] = to;
         }
-        if (S == 1) store(m, lane, v);
-        else s_sum[m * GV_ROWS + lane] = v;
-      }
-      if (S > 1) {                                           // one team per CTA
-        cluster_sync();
-        const uint32_t su = smem_u32(s_sum);
-        for (int o = tid * S + rank; o < nt_rows * GV_ROWS; o += THREADS * S) {
-          float v = 0.f;
-          for (int r = 0; r < S; ++r) v += lds32f_cluster(mapa_shared(su + o * 4, r));
-          store(o / GV_ROWS, o % GV_ROWS, v);
+        // the blocks' columns of a token add up to its sum, which then takes its place among the tokens' columns
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              float v0 = acc[a][b][i], v1 = acc[a][b][i + 1];
+              if constexpr (P > 1) {
+                v0 += v1;                                  // P = 2: lane t has token t
+                if constexpr (P == 4) v0 += __shfl_xor_sync(0xffffffffu, v0, 1);   // lanes 2m, 2m + 1 have token m
+                v1 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 2 : min(2 * t + 1, 3)));
+                v0 = __shfl_sync(0xffffffffu, v0, (lane & ~3) | (P == 4 ? 0 : min(2 * t, 3)));
+              }
+              acc[a][b][i] = v0 + accw[a][b][i];
+              acc[a][b][i + 1] = v1 + accw[a][b][i + 1];
+            }
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int m = b * 8 + 2 * t + i;
+            if (m >= nt_rows) continue;
+            float* const x = reinterpret_cast<float*>(smem + to) + m * GV_ROWS + rg;
+            x[0 ^ t * 8] = acc[0][b][i];
+            x[8 ^ t * 8] = acc[0][b][2 + i];
+            x[16 ^ t * 8] = acc[1][b][i];
+            x[24 ^ t * 8] = acc[1][b][2 + i];
+          }
+        if (NT == 2) fence_proxy_async_smem();             // the next copy into this stage comes after
+        team_sync(1 + team, tw * 32);
+        // a lane sums 4 rows of a token over the team's warps (P = 4: over half of them, and two lanes meet);
+        // another warp's turn first in each unit
+        constexpr int HALVES = P == 4 ? 2 : 1, TOK = 4 / HALVES;
+        const int lr = (lane & 7) * 4, half = HALVES == 2 ? (lane >> 3) & 1 : 0;
+        for (int mb = j0 * TOK; mb < nt_rows; mb += tw * TOK) {
+          const int m = mb + (lane >> 3) / HALVES;
+          const int o = (m * GV_ROWS + (lr ^ (m >> 1 & 3) * 8)) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (m < nt_rows) {
+#pragma unroll 4
+            for (int w = team * tw + half; w < team * tw + tw; w += HALVES) {
+              const float4 x = *reinterpret_cast<const float4*>(smem + (NT == 1 ? red + w * gv_sums(NT) : at[w]) + o);
+              v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            }
+          }
+          if constexpr (HALVES == 2) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, 8);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, 8);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, 8);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, 8);
+          }
+          if (m < nt_rows && half == 0) {
+            if (S == 1) store4(p, GROUPED ? s_list[m] : tile0 + m, u, lr, v);
+            else *reinterpret_cast<float4*>(s_sum + m * GV_ROWS + lr) = v;
+          }
         }
-        cluster_sync();                                      // the others have read this CTA's sums
-      } else if (NT == 2) {
-        team_sync(1 + team, tw * 32);                        // the sums have been read
+        if (S > 1) {                                       // one team per CTA
+          cluster_sync();
+          const uint32_t su = smem_u32(s_sum);
+          for (int o = tid * S + rank; o < nt_rows * (GV_ROWS / 4); o += THREADS * S) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < S; ++r) {
+              const float4 x = lds128f_cluster(mapa_shared(su + o * 16, r));
+              v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            }
+            store4(p, tile0 + o / (GV_ROWS / 4), u, o % (GV_ROWS / 4) * 4, v);
+          }
+          cluster_sync();                                  // the others have read this CTA's sums
+        } else if (NT == 2) {
+          team_sync(1 + team, tw * 32);                    // the sums have been read
+        }
+        if (NT == 2) {
+          load_next(stage);
+          next_stage();
+        }
+        if (NT == 1) red = 2 * sm.red + NW * gv_sums(NT) - red;
+        off += items;
       }
-      if (NT == 2) {
-        load_next(stage);
-        next_stage();
-      }
-      if (NT == 1) red = 2 * sm.red + NW * gv_sums(NT) - red;
-      off += items;
-    }
-    if constexpr (!GROUPED) break;
-    __syncthreads();                                         // the list and the tokens are free again
+    };
+    if (NT == 2) run(std::integral_constant<int, 1>{});
+    else if (nt_rows <= 2) run(std::integral_constant<int, 4>{});
+    else if (nt_rows <= 4) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 1>{});
+    if (wa < wb) __syncthreads();                          // the list, the table and the tokens are free again
   }
   // after a timeout, copies still in flight get a moment to land before the shared memory is given up
   if (*reinterpret_cast<volatile int*>(&s_abort)) {
@@ -735,18 +779,18 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int V, int CH, in
   return e;
 }
 
-constexpr int GV_SMEM_MAX = 232448 - 8192;                   // 227 KB less the static part and a reserve
+constexpr int GV_SMEM_MAX = 232448 - 8192;                 // 227 KB less the static part and a reserve
 
-template <int V, int CH, int P, int NT, int NW, int ST, bool GROUPED>
-cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, int slots, int n_cta, cudaStream_t s) {
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaStream_t s) {
   static PerDeviceOnce attr_once;
   const cudaError_t ae = attr_once.run([] {
-    return cudaFuncSetAttribute(gemv_kernel<V, CH, P, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GV_SMEM_MAX);
   });
   if (ae != cudaSuccess) return ae;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_cta * p.S, slots, 1);
+  cfg.gridDim = dim3(p.n_cta * p.S, 1, 1);
   cfg.blockDim = dim3(NW * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -759,52 +803,41 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, int sl
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, P, NT, NW, ST, GROUPED>, maps, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED>, maps, p);
 }
 
-// The split of one call. CH, NT, NW and ST are the kernel's, mt the tokens of a pass.
-template <int CH, int P, int NT, int NW, int ST, bool GROUPED>
-cudaError_t launch_v(GemvParams p, int slots, int num_sms, cudaStream_t s) {
-  static const int tw_min = getenv("TWM") ? atoi(getenv("TWM")) : 4, tw_units = getenv("TWU") ? atoi(getenv("TWU")) : 2;
+// The split of one call. CH, NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Returns
+// cudaErrorInvalidValue, and launches nothing, where `try_only` and the tokens of a pass would not fit one CTA.
+template <int CH, int NT, int NW, int ST, bool GROUPED>
+cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int V = p.G == 16 ? 16 : 32;
   const int chunks = p.K / CH;
   const int n_table = p.L ? p.K / p.G * p.R : 0;
-  GemvMaps maps;
-  cudaError_t e = encode_gemv_maps(&maps, p, V, CH, GROUPED ? p.E : 1);
-  if (e != cudaSuccess) return e;
   auto smem_of = [&](int S) {
     p.kc = (chunks + S - 1) / S * CH;
     return gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
   };
-  // parts of K: enough for the tokens to fit, and to fill the SMs where units are few
-  p.S = std::max(1, std::min({8, num_sms / std::max(1, p.n_units * slots), chunks / NW}));
+  // parts of K: to fill the SMs where units are few, and for the tokens to fit
+  const int max_s = GROUPED ? 1 : 8;
+  p.S = std::max(1, std::min({max_s, num_sms / std::max(1, p.n_units * ((p.M + p.mt - 1) / p.mt)), chunks / NW}));
   while (smem_of(p.S) > GV_SMEM_MAX) {
-    if (p.S < 8 && chunks / (p.S + 1) >= NW) ++p.S;
+    if (try_only) return cudaErrorInvalidValue;
+    if (p.S < max_s && chunks / (p.S + 1) >= NW) ++p.S;
     else if (p.mt > 1) p.mt = (p.mt + 1) / 2;
     else return cudaErrorInvalidValue;
   }
   const int smem = smem_of(p.S);
   p.nc_base = chunks / p.S;
   p.nc_more = chunks % p.S;
-  // every warp of a team has an item of every unit; a cluster's CTAs are one team each
-  int tw = NW;
-  if (p.S == 1)
-    while (tw > chunks || (tw > tw_min && p.n_units >= tw_units * num_sms * NW / tw)) tw /= 2;
-  p.tw_shift = 0;
-  while ((1 << p.tw_shift) < tw) ++p.tw_shift;
-  const int per_sm = std::max(1, std::min(2048 / 32 / NW / 2, 232448 / (smem + 4096)));
-  const int teams = NW / tw;
-  int n_cta = std::max(1, per_sm * num_sms / p.S);
-  if (GROUPED) {
-    slots = std::min(p.M, p.E);
-    n_cta = std::max(1, (2 * per_sm * num_sms / p.S + slots - 1) / slots);
-  } else {
-    slots = (p.M + p.mt - 1) / p.mt;
-  }
-  n_cta = std::min(n_cta, (p.n_units + teams - 1) / teams);
-  p.n_cta = n_cta;
-  return V == 16 ? launch_t<16, CH, P, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s)
-                 : launch_t<32, CH, P, NT, NW, ST, GROUPED>(maps, p, smem, slots, n_cta, s);
+  p.work = (long long)p.n_units * ((p.M + p.mt - 1) / p.mt);
+  p.n_cta = std::max(1, num_sms / p.S);
+  // grouped: at most one pass per row
+  p.n_cta = (int)std::min<long long>(p.n_cta, GROUPED ? (long long)p.n_units * p.M : p.work);
+  GemvMaps maps;
+  const cudaError_t e = encode_gemv_maps(&maps, p, V, CH, GROUPED ? p.E : 1);
+  if (e != cudaSuccess) return e;
+  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED>(maps, p, smem, s)
+                 : launch_t<32, CH, NT, NW, ST, GROUPED>(maps, p, smem, s);
 }
 
 }  // namespace
@@ -815,32 +848,16 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   p.g_shift = p.G == 16 ? 4 : p.G == 32 ? 5 : 6;
   p.rows32 = p.N % 32 == 0;
   if (p.expert) {
-    const int slots = std::min(p.M, p.E);
-    if (p.M <= 16) {
-      p.mt = std::min(p.M, 2);
-      return launch_v<256, 4, 1, 8, 2, true>(p, slots, num_sms, s);
-    }
-    if (p.M <= 128) {
-      p.mt = std::min(p.M, 8);
-      return launch_v<256, 1, 1, 8, 2, true>(p, slots, num_sms, s);
-    }
-    p.mt = 16;
-    return launch_v<256, 1, 2, 8, 2, true>(p, slots, num_sms, s);
-  }
-  if (p.M <= 2) {
-    p.mt = p.M;
-    return launch_v<256, 4, 1, 16, 2, false>(p, 1, num_sms, s);
-  }
-  if (p.M <= 4) {
-    p.mt = p.M;
-    return launch_v<256, 2, 1, 16, 2, false>(p, 1, num_sms, s);
+    p.mt = std::min(p.M, 8);
+    return launch_v<256, 1, 16, 2, true>(p, false, num_sms, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    return launch_v<256, 1, 1, 8, 3, false>(p, 1, num_sms, s);
+    const cudaError_t e = launch_v<256, 1, 16, 2, false>(p, true, num_sms, s);
+    return e != cudaErrorInvalidValue ? e : launch_v<256, 1, 8, 3, false>(p, false, num_sms, s);
   }
   p.mt = std::min(p.M, 16);
-  return launch_v<256, 1, 2, 8, 2, false>(p, 1, num_sms, s);
+  return launch_v<256, 2, 8, 2, false>(p, false, num_sms, s);
 }
 
 }  // namespace osc

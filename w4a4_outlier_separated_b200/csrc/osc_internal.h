@@ -102,7 +102,8 @@ struct GemvParams {
   const int* expert;       // grouped: M expert ids (device); nullptr = dense
   int fan, E;              // grouped: row r reads X row r / fan
   // set by the launcher
-  int S, n_cta, n_units, mt, kc, nc_base, nc_more, tw_shift, g_shift, rows32;
+  int S, n_cta, n_units, mt, kc, nc_base, nc_more, g_shift, rows32;
+  long long work;          // units of all passes (dense)
 };
 struct GemvMaps {
   CUtensorMap w, s, wl;
