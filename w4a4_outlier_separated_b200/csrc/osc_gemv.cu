@@ -39,7 +39,15 @@ template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrive on an mbarrier when this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+// One contiguous run of bytes (a multiple of 16, both ends aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
 
 __device__ __forceinline__ float4 lds128f_cluster(uint32_t a) {
   float4 v;
@@ -171,17 +179,19 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 }  // namespace
 
-// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp.
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp; TWO: the
+// passes have one or two tokens.
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED, bool TWO>
 __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ uint64_t s_full[NW][ST];   // a stage's data has arrived
+  __shared__ uint64_t s_xbar;           // the tokens have arrived
   __shared__ int s_abort;
   __shared__ int s_scan[2][NW];
   __shared__ int s_cols[2];             // first W_L column of this CTA's K range, one past the last
   __shared__ int s_list[16];            // the segment's rows of Y (grouped)
-  __shared__ int s_seg[5];              // the segment's expert, first row of its pass, rows, first unit; all work
+  __shared__ int s_seg[3];              // the segment's expert, rows, first row of its pass (grouped)
   __shared__ __align__(16) float s_sum[GV_ROWS * 8 * NT];
   constexpr int THREADS = NW * 32;
   constexpr int SLOT = 32 / V;                             // scale slots of 32 channels
@@ -209,105 +219,144 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   if (tid < 16) reinterpret_cast<uint32_t*>(smem + sm.zero)[tid] = 0u;
   if (lane == 0) {
     s_abort = 0;
-    for (int i = 0; i < ST; ++i) mbar_init(bars + i * 8, 1);
+    for (int i = 0; i < ST; ++i) mbar_init(bars + i * 8, 33);   // the copying lane, and each lane's scales
+    if (warp == 0) mbar_init(smem_u32(&s_xbar), NW);
     fence_barrier_init();
     if (warp == 0) {
       tma_prefetch_desc(&maps.w);
-      tma_prefetch_desc(&maps.s);
       if (n_table) tma_prefetch_desc(&maps.wl);
     }
   }
-  __syncwarp();
+  __syncthreads();
 
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the rows of each expert (grouped)
+  // ---- the rows of each expert (grouped); up to 32 rows every warp finds them by itself, lane r for row r
   int* const ids = reinterpret_cast<int*>(smem + sm.ids);
   int* const cnt = reinterpret_cast<int*>(smem + sm.cnt);
+  const bool small = GROUPED && p.M <= 32;
+  unsigned same = 0;                                       // small: the rows of this lane's expert
+  int my_id = -1, my_pass = 0;                             // and where it is the first, passes up to and with its own
+  long long w_each = p.w_each, w_more = p.w_more;
   if constexpr (GROUPED) {
-    for (int i = tid; i < p.E; i += THREADS) cnt[i] = 0;
-    __syncthreads();
-    for (int r = tid; r < p.M; r += THREADS) {
-      const int id = p.expert[r];
-      ids[r] = id;
-      if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
-      else if (id >= p.E && cta == 0) record_status(p.status, DEV_BAD_TABLE);
+    int passes;
+    if (small) {
+      if (lane < p.M) my_id = p.expert[lane];
+      if (my_id >= p.E) {
+        if (cta == 0 && warp == 0) record_status(p.status, DEV_BAD_TABLE);
+        my_id = -1;
+      }
+      same = __match_any_sync(0xffffffffu, max(my_id, -1));
+      my_pass = my_id >= 0 && __ffs(same) - 1 == lane ? (__popc(same) + p.mt - 1) / p.mt : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, my_pass, o);
+        if (lane >= o) my_pass += x;
+      }
+      passes = __shfl_sync(0xffffffffu, my_pass, 31);
+    } else {
+      for (int i = tid; i < p.E; i += THREADS) cnt[i] = 0;
+      __syncthreads();
+      for (int r = tid; r < p.M; r += THREADS) {
+        const int id = p.expert[r];
+        ids[r] = id;
+        if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
+        else if (id >= p.E && cta == 0) record_status(p.status, DEV_BAD_TABLE);
+      }
+      __syncthreads();
+      int n = 0;
+      for (int i = tid; i < p.E; i += THREADS) n += (cnt[i] + p.mt - 1) / p.mt;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) s_scan[0][warp] = n;
+      __syncthreads();
+      passes = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[0][lane] : 0);
     }
-    __syncthreads();
     // rows without an expert come out as zeros
     for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
-      if (ids[r] >= 0 && ids[r] < p.E) continue;
+      const int id = small ? __shfl_sync(0xffffffffu, my_id, r) : ids[r];
+      if (id >= 0 && id < p.E) continue;
       for (int n = tid; n < N; n += THREADS) {
         p.Y[(size_t)r * N + n] = 0;
         if (p.Yf32) p.Yf32[(size_t)r * N + n] = 0.f;
       }
     }
-    if (warp == 0) {
-      int passes = 0;
-      for (int i = lane; i < p.E; i += 32) passes += (cnt[i] + p.mt - 1) / p.mt;
-      passes = __reduce_add_sync(0xffffffffu, passes);
-      if (lane == 0) s_seg[4] = passes * p.n_units;
+    const long long total = (long long)passes * p.n_units;
+    if (total <= 0x7FFFFFFF) {
+      w_each = (unsigned)total / (unsigned)p.n_cta;
+      w_more = (unsigned)total % (unsigned)p.n_cta;
+    } else {
+      w_each = total / p.n_cta;
+      w_more = total % p.n_cta;
     }
-    __syncthreads();
   }
   // this CTA's run of the work
-  const long long total = GROUPED ? s_seg[4] : p.work;
-  long long wa = total * cta / p.n_cta;
-  const long long wb = total * (cta + 1) / p.n_cta;
+  long long wa = cta * w_each + min((long long)cta, w_more);
+  const long long wb = wa + w_each + (cta < w_more ? 1 : 0);
 
   int stage = 0;                                           // of the next item to use
-  uint32_t parity = 0;                                     // of its barrier
+  uint32_t parity = 0, xparity = 0;                        // of its barrier, of the tokens'
   bool dead = false;                                       // a wait ran out
   while (wa < wb) {
     // ---- the segment: units u0 .. u1 - 1 of one pass over expert e
-    int e = 0, tile0, nt_rows, u0;
-    if constexpr (GROUPED) {
-      if (warp == 0) {
-        // the expert whose passes hold unit wa of the work
-        int at = (int)(wa / p.n_units), b = 0, first = 0;
-        for (;; b += 32) {
-          const int c = b + lane < p.E ? (cnt[b + lane] + p.mt - 1) / p.mt : 0;
-          int sum = c;                                     // inclusive over the lanes
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
-          }
-          const unsigned m = __ballot_sync(0xffffffffu, at < sum);
-          if (m) {
-            const int l = __ffs(m) - 1;
-            e = b + l;
-            first = (at - __shfl_sync(0xffffffffu, sum - c, l)) * p.mt;
-            break;
-          }
-          at -= __shfl_sync(0xffffffffu, sum, 31);
-        }
-        // its rows first .. first + mt - 1, in ascending order
-        int have = -first;
-        for (int r = 0; r < p.M && have < p.mt; r += 32) {
-          const bool hit = r + lane < p.M && ids[r + lane] == e;
-          const unsigned m = __ballot_sync(0xffffffffu, hit);
-          const int i = have + __popc(m & ((1u << lane) - 1u));
-          if (hit && i >= 0 && i < p.mt) s_list[i] = r + lane;
-          have += __popc(m);
-        }
-        if (lane == 0) {
-          s_seg[0] = e;
-          s_seg[2] = min(have, p.mt);
-          s_seg[3] = (int)(wa % p.n_units);
-        }
-      }
-      __syncthreads();
-      e = s_seg[0];
-      tile0 = 0;
-      nt_rows = s_seg[2];
-      u0 = s_seg[3];
-    } else {
-      const int pass = p.work == p.n_units ? 0 : (int)(wa / p.n_units);
+    int e = 0, tile0 = 0, nt_rows, pass = 0;
+    if (wa >= p.n_units) pass = wa <= 0x7FFFFFFF ? (int)((unsigned)wa / (unsigned)p.n_units) : (int)(wa / p.n_units);
+    const int u0 = (int)(wa - (long long)pass * p.n_units);
+    if constexpr (!GROUPED) {
       tile0 = pass * p.mt;
       nt_rows = min(p.mt, p.M - tile0);
-      u0 = (int)(wa - (long long)pass * p.n_units);
+    } else if (small) {
+      const int l = __ffs(__ballot_sync(0xffffffffu, pass < my_pass)) - 1;
+      const unsigned rows = __shfl_sync(0xffffffffu, same, l);
+      e = __shfl_sync(0xffffffffu, my_id, l);
+      const int n = __popc(rows), before = __shfl_sync(0xffffffffu, my_pass, l) - (n + p.mt - 1) / p.mt;
+      const int first = (pass - before) * p.mt, i = __popc(rows & ((1u << lane) - 1u)) - first;
+      nt_rows = min(n - first, p.mt);
+      if (rows >> lane & 1 && i >= 0 && i < p.mt) s_list[i] = lane;   // the same from every warp
+      __syncwarp();
+    } else {
+      // the expert that has pass number `pass`: 32 experts a warp at a time
+      int before = 0;
+      for (int b = 0;; b += THREADS) {
+        const int c = b + tid < p.E ? (cnt[b + tid] + p.mt - 1) / p.mt : 0;
+        const int sum = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) s_scan[1][warp] = sum;
+        __syncthreads();
+        const int x = lane < NW ? s_scan[1][lane] : 0;
+        const int low = before + __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+        if (pass >= low && pass < low + sum) {
+          int up = c;                                      // inclusive over the lanes
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += y;
+          }
+          if (pass >= low + up - c && pass < low + up) {
+            s_seg[0] = b + tid;
+            s_seg[1] = min(cnt[b + tid] - (pass - low - up + c) * p.mt, p.mt);
+            s_seg[2] = (pass - low - up + c) * p.mt;
+          }
+        }
+        before += __reduce_add_sync(0xffffffffu, x);
+        __syncthreads();
+        if (pass < before) break;
+      }
+      e = s_seg[0];
+      nt_rows = s_seg[1];
+      // its rows first .. first + nt_rows - 1, in ascending order
+      const int first = s_seg[2];
+      int have = -first;
+      for (int r = 0, it = 0; r < p.M && have < nt_rows; r += THREADS, it ^= 1) {
+        const bool hit = r + tid < p.M && ids[r + tid] == e;
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        if (lane == 0) s_scan[it][warp] = __popc(m);
+        __syncthreads();
+        const int x = lane < NW ? s_scan[it][lane] : 0;
+        const int i = have + __reduce_add_sync(0xffffffffu, lane < warp ? x : 0) + __popc(m & ((1u << lane) - 1u));
+        if (hit && i >= 0 && i < nt_rows) s_list[i] = r + tid;
+        have += __reduce_add_sync(0xffffffffu, x);
+      }
+      __syncthreads();
     }
     const int u1 = (int)min((long long)p.n_units, u0 + (wb - wa));
     wa += u1 - u0;
@@ -320,20 +369,22 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     const int tw = 1 << tw_shift, teams = NW >> tw_shift, team = warp >> tw_shift, twarp = warp & (tw - 1);
     const int8_t* const L = p.L + (size_t)e * n_table;
     const int wrow0 = GROUPED ? e * N : 0;                 // the expert's first row of QW and W_L
-    const int sblk0 = GROUPED ? e * ((N + 127) / 128) : 0; // and 128-row block of SW
+    // the lane's 16 bytes of an item's scales: atom lane / 8 of it, row lane % 8 of each octet
+    const int satoms = K / V / 4;
+    const uint8_t* const sfrom = p.SW + ((size_t)(GROUPED ? e * ((N + 127) / 128) : 0) * satoms +
+                                         (size_t)c0 * (CH / V / 4) + (lane >> 3)) * 512 + (lane & 7) * 16;
     auto xrow = [&](int m) -> const uint16_t* {
       if constexpr (GROUPED) return p.X + (size_t)(s_list[m] / p.fan) * K;
       else return p.X + (size_t)(tile0 + m) * K;
     };
 
-    // ---- what the rest waits for first: the table, and the tokens as they are (each warp the items
-    // it will convert)
+    // ---- what the rest waits for first: the table, and the tokens as they are (one copy each)
     const int8_t l_first = tid < n_table ? L[tid] : -1;
-    for (int c = warp; c < nc; c += NW)
-#pragma unroll 4
-      for (int m = 0; m < nt_rows; ++m)
-        cp_async<XB>(sbase + sm.x + m * p.kc * 2 + c * CH * 2 + ((lane * XB) ^ ((m & 1) << 6)),
-                     xrow(m) + (size_t)(c0 + c) * CH + lane * (CH / 32));
+    if (lane == 0) {
+      const uint32_t xbar = smem_u32(&s_xbar), bytes = nc * CH * 2;
+      mbar_arrive_expect_tx(xbar, max(0, (nt_rows - warp + NW - 1) / NW) * bytes);
+      for (int m = warp; m < nt_rows; m += NW) bulk_load(sbase + sm.x + m * p.kc * 2, xrow(m) + (size_t)c0 * CH, bytes, xbar);
+    }
 
     // ---- start the weight stream: the next item to load is pj of unit pu. Items 0 .. nc - 1 of a
     // unit are codes; the W_L columns' items follow, known only after the table has been read. The
@@ -354,7 +405,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         const bool main = pj < nc;
         const CUtensorMap* const m = main ? &maps.w : &maps.wl;
         const int x = main ? (c0 + pj) * RB : (w0 + pj - nc) * COLS;
-        mbar_arrive_expect_tx(bar, main ? GV_ROWS * RB + SBYTES : GV_ROWS * RB);
+        mbar_arrive_expect_tx(bar, GV_ROWS * RB);
         // octet q: rows 32 q + 8 (pu % 4) .. + 7 of the 128-row block
         if (p.rows32) {
           tma_load_3d(sw, m, x, (pu & 3) * 8, (wrow0 >> 5) + (pu >> 2) * 4, bar);
@@ -363,8 +414,11 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           for (int q = 0; q < 4; ++q)
             tma_load_3d(sw + q * 8 * RB, m, x, wrow0 + (pu >> 2) * 128 + q * 32 + (pu & 3) * 8, 0, bar);
         }
-        if (main) tma_load_3d(sbase + sscale + to * SBYTES, &maps.s, (pu & 3) * 32, (c0 + pj) * (CH / V / 4), sblk0 + (pu >> 2), bar);
       }
+      if (pj < nc && lane * 16 < SBYTES)
+        cp_async<16>(sbase + sscale + to * SBYTES + lane * 16,
+                     sfrom + ((size_t)(pu >> 2) * satoms + (size_t)pj * (CH / V / 4)) * 512 + (pu & 3) * 128);
+      cp_async_arrive(bars + to * 8);
       pj += tw;
       if (pj >= items) settle();
     };
@@ -413,9 +467,10 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     if (pj >= items) settle();
 
     // ---- stage the tokens: protected channels apart, the rest as f16 with a power of two per token and item,
-    // in place (16-byte pieces of odd tokens trade places in fours, so that two tokens' 64 bytes meet
+    // in place (16-byte pieces of odd tokens trade places in fours, so that two tokens' 64 bytes will meet
     // different banks)
-    cp_async_wait_all();
+    mbar_wait(smem_u32(&s_xbar), xparity, &s_abort, p.status);
+    xparity ^= 1;
     auto convert = [&](auto mb) {
       constexpr int MB = decltype(mb)::value;              // tokens at a time, for their latencies' sake
       for (int c = warp; c < nc; c += NW) {
@@ -427,7 +482,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
 #pragma unroll
           for (int y = 0; y < MB; ++y) {
             const int m = MB == 1 ? m0 : min(m0 + y, nt_rows - 1);
-            const uint8_t* const x = xc + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6));
+            const uint8_t* const x = xc + m * p.kc * 2 + lane * XB;
             if constexpr (XB == 8) {
               const uint2 q = *reinterpret_cast<const uint2*>(x);
               v[y][0] = q.x; v[y][1] = q.y;
@@ -481,7 +536,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         }
       }
     };
-    if (nt_rows <= 2) convert(std::integral_constant<int, 1>{});
+    if (TWO || nt_rows <= 2) convert(std::integral_constant<int, 1>{});
     else convert(std::integral_constant<int, 4>{});
 #pragma unroll 1
     for (; pre < ST; ++pre) {
@@ -742,10 +797,13 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       }
     };
     if (NT == 2) run(std::integral_constant<int, 1>{});
-    else if (nt_rows <= 2) run(std::integral_constant<int, 4>{});
+    else if (TWO || nt_rows <= 2) run(std::integral_constant<int, 4>{});
     else if (nt_rows <= 4) run(std::integral_constant<int, 2>{});
     else run(std::integral_constant<int, 1>{});
-    if (wa < wb) __syncthreads();                          // the list, the table and the tokens are free again
+    if (wa < wb) {
+      fence_proxy_async_smem();                            // the next tokens' copies come after
+      __syncthreads();                                     // the list, the table and the tokens are free again
+    }
   }
   // after a timeout, copies still in flight get a moment to land before the shared memory is given up
   if (*reinterpret_cast<volatile int*>(&s_abort)) {
@@ -756,11 +814,11 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
 
 namespace {
 
-// Tensor maps of the weight's parts, one copy of an item each. Rows as (32 rows) x (blocks of 32), so
+// Tensor maps of the codes and of W_L, one copy of an item each. Rows as (32 rows) x (blocks of 32), so
 // that one box {a row's bytes, 8 rows, 4 blocks} is a unit's four octets; where N is not a multiple of
 // 32 as one run of rows, a box of 8. Swizzled by the row length, so that 8 rows' equal pieces meet
-// different banks. Scales as (128 words of an atom) x (atoms along K) x (128-row blocks).
-cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int V, int CH, int E) {
+// different banks.
+cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int CH, int E) {
   const uint64_t rows = (uint64_t)E * p.N;
   const CUtensorMapSwizzle sw = CH == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   auto operand = [&](CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t width, uint64_t pitch, uint32_t box) {
@@ -772,20 +830,16 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int V, int CH, in
   cudaError_t e = operand(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.QW, (uint64_t)p.K / 2, (uint64_t)p.K / 2, CH / 2);
   if (e == cudaSuccess && p.L && p.K_L)
     e = operand(&m->wl, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.WL, (uint64_t)p.K_L, (uint64_t)p.K_L * 2, CH / 4);
-  const uint64_t atoms = (uint64_t)p.K / V / 4;
-  const uint64_t d[3] = {128, atoms, (uint64_t)E * ((p.N + 127) / 128)}, st[2] = {512, atoms * 512};
-  const uint32_t box[3] = {32, (uint32_t)(CH / V / 4), 1};
-  if (e == cudaSuccess) e = encode_map(&m->s, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, p.SW, d, st, box, CU_TENSOR_MAP_SWIZZLE_NONE);
   return e;
 }
 
 constexpr int GV_SMEM_MAX = 232448 - 8192;                 // 227 KB less the static part and a reserve
 
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED>
+template <int V, int CH, int NT, int NW, int ST, bool GROUPED, bool TWO>
 cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaStream_t s) {
   static PerDeviceOnce attr_once;
   const cudaError_t ae = attr_once.run([] {
-    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GV_SMEM_MAX);
   });
   if (ae != cudaSuccess) return ae;
@@ -803,12 +857,12 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaSt
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED>, maps, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED, TWO>, maps, p);
 }
 
 // The split of one call. CH, NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Returns
 // cudaErrorInvalidValue, and launches nothing, where `try_only` and the tokens of a pass would not fit one CTA.
-template <int CH, int NT, int NW, int ST, bool GROUPED>
+template <int CH, int NT, int NW, int ST, bool GROUPED, bool TWO = false>
 cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int V = p.G == 16 ? 16 : 32;
   const int chunks = p.K / CH;
@@ -829,15 +883,17 @@ cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int smem = smem_of(p.S);
   p.nc_base = chunks / p.S;
   p.nc_more = chunks % p.S;
-  p.work = (long long)p.n_units * ((p.M + p.mt - 1) / p.mt);
+  const long long work = (long long)p.n_units * ((p.M + p.mt - 1) / p.mt);
   p.n_cta = std::max(1, num_sms / p.S);
   // grouped: at most one pass per row
-  p.n_cta = (int)std::min<long long>(p.n_cta, GROUPED ? (long long)p.n_units * p.M : p.work);
+  p.n_cta = (int)std::min<long long>(p.n_cta, GROUPED ? (long long)p.n_units * p.M : work);
+  p.w_each = work / p.n_cta;
+  p.w_more = work % p.n_cta;
   GemvMaps maps;
-  const cudaError_t e = encode_gemv_maps(&maps, p, V, CH, GROUPED ? p.E : 1);
+  const cudaError_t e = encode_gemv_maps(&maps, p, CH, GROUPED ? p.E : 1);
   if (e != cudaSuccess) return e;
-  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED>(maps, p, smem, s)
-                 : launch_t<32, CH, NT, NW, ST, GROUPED>(maps, p, smem, s);
+  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s)
+                 : launch_t<32, CH, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s);
 }
 
 }  // namespace
@@ -853,7 +909,8 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    const cudaError_t e = launch_v<256, 1, 16, 2, false>(p, true, num_sms, s);
+    const cudaError_t e = p.M <= 2 ? launch_v<256, 1, 16, 2, false, true>(p, true, num_sms, s)
+                                   : launch_v<256, 1, 16, 2, false>(p, true, num_sms, s);
     return e != cudaErrorInvalidValue ? e : launch_v<256, 1, 8, 3, false>(p, false, num_sms, s);
   }
   p.mt = std::min(p.M, 16);

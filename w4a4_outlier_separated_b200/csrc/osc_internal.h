@@ -103,10 +103,10 @@ struct GemvParams {
   int fan, E;              // grouped: row r reads X row r / fan
   // set by the launcher
   int S, n_cta, n_units, mt, kc, nc_base, nc_more, g_shift, rows32;
-  long long work;          // units of all passes (dense)
+  long long w_each, w_more;   // units of each CTA, CTAs with one more (dense)
 };
 struct GemvMaps {
-  CUtensorMap w, s, wl;
+  CUtensorMap w, wl;
 };
 // Tiled tensor map over a row-major tensor; dims[0] is the contiguous dimension (rank <= 3).
 cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
