@@ -360,11 +360,22 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     }
     const int u1 = (int)min((long long)p.n_units, u0 + (wb - wa));
     wa += u1 - u0;
-    // teams: as many as four where there are units for them; every warp of a team has items of every unit
-    int tw_shift = 31 - __clz(NW);
+    // teams of tw warps: the fewest rounds over the teams, a round costing a warp's items and about OV / 4 more for
+    // their sums; every warp of a team has items of every unit, and a cluster's CTAs are one team each
+    constexpr int LOG_NW = NW == 16 ? 4 : 3, OV = 2;
+    static_assert(NW == 1 << LOG_NW, "warps");
+    int tw_shift = LOG_NW;
     if (S == 1) {
-      tw_shift -= u1 - u0 >= 4 ? 2 : u1 - u0 >= 2 ? 1 : 0;
-      while ((1 << tw_shift) > nc) --tw_shift;
+      const int nu = u1 - u0, n = nc + (n_table ? (min(p.K_L, n_table) + COLS - 1) / COLS : 0);
+      int best = 0x7FFFFFFF;
+#pragma unroll
+      for (int i = LOG_NW; i >= 0; --i) {
+        const int cost = ((nu + (NW >> i) - 1) >> (LOG_NW - i)) * (4 * ((n + (1 << i) - 1) >> i) + OV);
+        if (1 << i <= nc && cost < best) {
+          best = cost;
+          tw_shift = i;
+        }
+      }
     }
     const int tw = 1 << tw_shift, teams = NW >> tw_shift, team = warp >> tw_shift, twarp = warp & (tw - 1);
     const int8_t* const L = p.L + (size_t)e * n_table;
