@@ -12,7 +12,7 @@
 //
 // Work split: 8 consecutive channels per thread and step (one 16-byte load of each input, one
 // 8-byte store of codes), four neighbouring threads to a 32-channel block, whole warps to a
-// row, so that the block maximum and the four scale bytes of a layout word meet by shuffles.
+// row, so that the block maximum meets by shuffles.
 #include "osc_device.cuh"
 #include "osc_internal.h"
 
@@ -27,49 +27,118 @@ __device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Two fp32 values in one 64-bit register: the packed operations round each half as the scalar ones do.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2f(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, f2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t bf16x2(f2 v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4]) {
+  return make_uint4(bf16x2(f[0]), bf16x2(f[1]), bf16x2(f[2]), bf16x2(f[3]));
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+// Four E4M3 codes, low byte first.
+__device__ __forceinline__ uint32_t e4m3x4(f2 a, f2 b) {
+  float x, y, z, w;
+  unpack2(a, x, y);
+  unpack2(b, z, w);
   uint32_t r;
   asm("{\n\t.reg .b16 l, h;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
       "mov.b32 %0, {l, h};\n\t}"
-      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+      : "=r"(r) : "f"(x), "f"(y), "f"(z), "f"(w));
   return r;
+}
+
+// What follows the sum of squares of a row, for the calling thread's 8 channels of step `ch`: the normed values,
+// their block's exponent, the codes and (one lane in four) the scale. A warp's lanes hold consecutive steps.
+__device__ __forceinline__ void norm_quant8(const AddNormParams& p, size_t base, uint8_t* srow, int ch, const f2 (&h)[4],
+                                            f2 inv2, const uint4& gamma) {
+  const int lane = threadIdx.x & 31;
+  f2 g[4], y[4];
+  unpack8(gamma, g);
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i] = mul2f(mul2f(h[i], inv2), g[i]);
+    float lo, hi;
+    unpack2(y[i], lo, hi);
+    am = fmaxf(am, fmaxf(fabsf(lo), fabsf(hi)));
+  }
+  if (p.Y) *reinterpret_cast<uint4*>(p.Y + base + (size_t)ch * 8) = pack8(y);
+  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+  // the exponent e = floor(log2 amax) - 8, at least -127 (also for a zero or subnormal block), as its byte e + 127
+  const int byte = max((int)(__float_as_uint(am) >> 23) - 8, 0);
+  const float f = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: the product is exact
+  const f2 ff = pack2(f, f);
+  const uint2 q = make_uint2(e4m3x4(mul2f(y[0], ff), mul2f(y[1], ff)), e4m3x4(mul2f(y[2], ff), mul2f(y[3], ff)));
+  *reinterpret_cast<uint2*>(p.Q + base + (size_t)ch * 8) = q;
+  // one byte of each four lanes; a layout word's four bytes meet in one write of the warp
+  if ((lane & 3) == 0) srow[(size_t)(ch >> 4) * 512 + ((ch >> 2) & 3)] = (uint8_t)byte;
+}
+
+// The first scale word of a row (the next ones 512 bytes apart): atoms of 128 rows x 4 slots.
+__device__ __forceinline__ uint8_t* scale_row(const AddNormParams& p, int row) {
+  return p.S + (size_t)(row >> 7) * (p.K >> 7) * 512 + (size_t)((row & 31) * 16 + ((row >> 5) & 3) * 4);
+}
+
+// 1 / sqrt(ss / K + eps), within 2^-22 of it (the root's own error); an all-zero row with eps = 0 stays zero.
+__device__ __forceinline__ f2 inverse2(const AddNormParams& p, float ss) {
+  const float ms = ss * __frcp_rn((float)p.K) + p.eps;
+  const float inv = ms > 0.f ? rsqrtf(ms) : 0.f;
+  return pack2(inv, inv);
 }
 
 }  // namespace
 
-// C: steps of 8 channels per thread. A CTA holds p.rows_per_cta rows of `tpr` threads each.
-// Rows M .. (next multiple of 128) only write zero scales.
-template <int C>
+// C: steps of 8 channels per thread; RES: there is a residual. A CTA holds p.rows_per_cta rows of `tpr`
+// threads each. Rows M .. (next multiple of 128) only write zero scales.
+template <int C, bool RES>
 __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, int tpr) {
   __shared__ float part[32];
   const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * p.rows_per_cta + sub;
-  const int nchunk = p.K >> 3, nslot4 = p.K >> 7;
+  const int nchunk = p.K >> 3;
   const bool live = row < p.M;
   const size_t base = (size_t)row * p.K;
-  // the scale word of four blocks: 512-byte atoms of 128 rows x 4 slots
-  uint8_t* const srow = p.S + (size_t)(row >> 7) * nslot4 * 512 + (size_t)((row & 31) * 16 + ((row >> 5) & 3) * 4);
+  uint8_t* const srow = scale_row(p, row);
 
   grid_dep_wait();
   grid_dep_launch();
-  float h[C][8];
-  float ss = 0.f;
+  f2 h[C][4];
+  f2 ss2 = pack2(0.f, 0.f);
   if (live) {
     uint4 a[C], b[C];
 #pragma unroll
@@ -77,7 +146,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
       const int ch = c * tpr + t;
       if (ch < nchunk) {
         a[c] = load_stream(p.X + base + (size_t)ch * 8);
-        if (p.res) b[c] = load_stream(p.res + base + (size_t)ch * 8);
+        if (RES) b[c] = load_stream(p.res + base + (size_t)ch * 8);
       }
     }
 #pragma unroll
@@ -85,18 +154,21 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
       const int ch = c * tpr + t;
       if (ch < nchunk) {
         unpack8(a[c], h[c]);
-        if (p.res) {
-          float r[8];
+        if (RES) {
+          f2 r[4];
           unpack8(b[c], r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+          for (int i = 0; i < 4; ++i) h[c][i] = add2(h[c][i], r[i]);
         }
         if (p.H) *reinterpret_cast<uint4*>(p.H + base + (size_t)ch * 8) = pack8(h[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
+        for (int i = 0; i < 4; ++i) ss2 = fma2(h[c][i], h[c][i], ss2);
       }
     }
   }
+  float ss, odd;
+  unpack2(ss2, ss, odd);
+  ss += odd;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const int wpr = tpr >> 5;
@@ -108,41 +180,20 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
   }
   if (!live) {
     if (row < ((p.M + 127) & ~127))
-      for (int s = t; s < nslot4; s += tpr) *reinterpret_cast<uint32_t*>(srow + (size_t)s * 512) = 0u;
+      for (int s = t; s < (p.K >> 7); s += tpr) *reinterpret_cast<uint32_t*>(srow + (size_t)s * 512) = 0u;
     return;
   }
-  const float ms = ss / (float)p.K + p.eps;
-  const float inv = ms > 0.f ? 1.0f / sqrtf(ms) : 0.f;   // an all-zero row with eps = 0 stays zero
+  const f2 inv2 = inverse2(p, ss);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int ch = c * tpr + t;
     if (ch >= nchunk) break;                             // the same for a whole warp
-    float g[8], y[8];
-    unpack8(*reinterpret_cast<const uint4*>(p.gamma + (size_t)ch * 8), g);
-    float am = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] = (h[c][i] * inv) * g[i];
-      am = fmaxf(am, fabsf(y[i]));
-    }
-    if (p.Y) *reinterpret_cast<uint4*>(p.Y + base + (size_t)ch * 8) = pack8(y);
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    // floor(log2 amax) - 8 from the exponent field, at least -127 (also for a zero or subnormal block)
-    const int e = max((int)(__float_as_uint(am) >> 23) - 127 - 8, -127);
-    const float f = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e: the product is exact
-    const uint2 q = make_uint2(e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
-                               e4m3x4(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
-    *reinterpret_cast<uint2*>(p.Q + base + (size_t)ch * 8) = q;
-    uint32_t s = (uint32_t)(e + 127) << (((lane >> 2) & 3) * 8);
-    s |= __shfl_xor_sync(0xffffffffu, s, 4);
-    s |= __shfl_xor_sync(0xffffffffu, s, 8);
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(srow + (size_t)(ch >> 4) * 512) = s;
+    norm_quant8(p, base, srow, ch, h[c], inv2, *reinterpret_cast<const uint4*>(p.gamma + (size_t)ch * 8));
   }
 }
 
-template <int C>
-static cudaError_t launch_c(AddNormParams p, int tpr, cudaStream_t s) {
+template <int C, bool RES>
+static cudaError_t launch_r(AddNormParams p, int tpr, cudaStream_t s) {
   p.rows_per_cta = std::max(1, 128 / tpr);
   cudaLaunchConfig_t cfg = {};
   const int mpad = (p.M + 127) / 128 * 128;
@@ -154,7 +205,12 @@ static cudaError_t launch_c(AddNormParams p, int tpr, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, add_rmsnorm_fp8_kernel<C>, p, tpr);
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_fp8_kernel<C, RES>, p, tpr);
+}
+
+template <int C>
+static cudaError_t launch_c(const AddNormParams& p, int tpr, cudaStream_t s) {
+  return p.res ? launch_r<C, true>(p, tpr, s) : launch_r<C, false>(p, tpr, s);
 }
 
 cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s) {
