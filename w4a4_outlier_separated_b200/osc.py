@@ -304,32 +304,36 @@ def osc_linear_grouped(QX, SX, B, QW, SW, WL, mblock_expert, kl, E: int, Mp: int
                                                           _stream(stream)))
 
 
-def _rows(name: str, t, n: int, device, itemsizes):
-    """Address of a dense CUDA tensor of n elements of an allowed size on `device` (None: None)."""
+# The decoding-step calls below check sizes, strides and devices of every operand: a step makes
+# them one at a time, so the checks are kept to three properties and one address per tensor.
+
+def _at(name: str, t, nbytes: int, device: int):
+    """Address of a contiguous tensor of nbytes on CUDA device `device` (None: None)."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if t.numel() != n or t.element_size() not in itemsizes:
-        raise ValueError(f"{name}: expected {n} elements of {itemsizes} bytes, got {t.numel()} of {t.element_size()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.nbytes != nbytes or t.get_device() != device or not t.is_contiguous():
+        if t.get_device() != device:
+            raise ValueError(f"{name}: expected a tensor on device {device}, got one on {t.device}")
+        raise ValueError(f"{name}: expected a contiguous tensor of {nbytes} bytes, got {t.nbytes}")
     return t.data_ptr()
 
 
-def _call_on(device, name: str, args, stream):
-    """Call lib().name(*args, stream) with `device` current (its current stream unless one is given)."""
-    if device.type != "cuda":
+def _launch(name: str, device: int, stream, args):
+    """Call the library's `name` on `stream`, or the current stream, of CUDA device `device`."""
+    if device < 0:
         raise ValueError("expected a CUDA tensor")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"expected a stream of {device}, got one of {stream.device}")
-    index = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"expected a stream of device {device}, got one of {stream.device}")
+    else:
+        raw = stream.cuda_stream
     fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+            rc = fn(*args, raw)
     if rc != OSC_OK:
         _check(name, rc)
 
@@ -338,21 +342,20 @@ def osc_add_rmsnorm_quantize_fp8(X, res, gamma, eps: float, H, Y, QX8, SX, strea
     """h = X + res (res None: X), y = RMSNorm(h) * gamma: MXFP8 codes and scales of y into QX8 and SX,
     bf16(h) into H and bf16(y) into Y where they are given. H may be X or res."""
     M, K = X.shape
-    d = X.device
+    d = X.get_device()
     n = M * K
-    _call_on(d, "osc_add_rmsnorm_quantize_fp8",
-             (_rows("X", X, n, d, (2,)), _rows("res", res, n, d, (2,)), _rows("gamma", gamma, K, d, (2,)), eps, M, K,
-              _rows("H", H, n, d, (2,)), _rows("Y", Y, n, d, (2,)), _rows("QX8", QX8, n, d, (1,)),
-              _rows("SX", SX, (M + 127) // 128 * 4 * K, d, (1,))), stream)
+    _launch("osc_add_rmsnorm_quantize_fp8", d, stream,
+            (_at("X", X, 2 * n, d), _at("res", res, 2 * n, d), _at("gamma", gamma, 2 * K, d), eps, M, K,
+             _at("H", H, 2 * n, d), _at("Y", Y, 2 * n, d), _at("QX8", QX8, n, d),
+             _at("SX", SX, (M + 127) // 128 * 4 * K, d)))
 
 
-def _gemv_operands(E: int, K: int, G: int, L, K_L: int, QW, SW, WL, N: int, d):
-    """(address of L, slots per group, addresses of QW, SW and WL) of E experts' prepared weights."""
-    V = 16 if G == 16 else 32
+def _weight_at(E: int, K: int, G: int, L, K_L: int, QW, SW, WL, N: int, d: int):
+    """(address of L, slots per group, K_L, addresses of QW, SW and WL) of E experts' prepared weights."""
     R = 1 if L is None else _slots(L, E * max(1, K // G))
-    return (_rows("L", L, E * (K // G) * R, d, (1,)), R, _rows("QW", QW, E * N * (K // 2), d, (1,)),
-            _rows("SW", SW, E * ((N + 127) // 128) * 128 * (K // V), d, (1,)),
-            _rows("WL", WL, E * N * K_L, d, (2,)) if K_L else None)
+    return (_at("L", L, E * (K // G) * R, d), R, K_L, _at("QW", QW, E * N * (K // 2), d),
+            _at("SW", SW, E * ((N + 127) // 128) * 128 * (K // (16 if G == 16 else 32)), d),
+            _at("WL", WL, 2 * E * N * K_L, d) if K_L else None)
 
 
 def osc_gemv(X, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
@@ -361,10 +364,10 @@ def osc_gemv(X, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=No
     if G not in (16, 32, 64):
         _check("osc_gemv", -3)
     M, K = X.shape
-    d = X.device
-    l, R, qw, sw, wl = _gemv_operands(1, K, G, L, K_L, QW, SW, WL, N, d)
-    _call_on(d, "osc_gemv", (_rows("X", X, M * K, d, (2,)), M, K, G, l, R, K_L, qw, sw, wl, N,
-                             _rows("Y", Y, M * N, d, (2,)), _rows("Yf32", Yf32, M * N, d, (4,))), stream)
+    d = X.get_device()
+    _launch("osc_gemv", d, stream,
+            (_at("X", X, 2 * M * K, d), M, K, G, *_weight_at(1, K, G, L, K_L, QW, SW, WL, N, d), N,
+             _at("Y", Y, 2 * M * N, d), _at("Yf32", Yf32, 4 * M * N, d)))
 
 
 def osc_gemv_grouped(X, fan: int, expert, E: int, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
@@ -375,13 +378,13 @@ def osc_gemv_grouped(X, fan: int, expert, E: int, G: int, L, K_L: int, QW, SW, W
     if expert.dtype != torch.int32:
         raise ValueError("expert: expected an int32 tensor")
     Mx, K = X.shape
-    rows, d = expert.numel(), X.device
+    rows, d = expert.numel(), X.get_device()
     if fan < 1 or Mx != (rows + fan - 1) // fan:
         raise ValueError(f"{rows} rows with fan {fan} need {-(-rows // max(1, fan))} rows of X, got {Mx}")
-    l, R, qw, sw, wl = _gemv_operands(E, K, G, L, K_L, QW, SW, WL, N, d)
-    _call_on(d, "osc_gemv_grouped", (_rows("X", X, Mx * K, d, (2,)), rows, fan, _rows("expert", expert, rows, d, (4,)), E, K,
-                                     G, l, R, K_L, qw, sw, wl, N, _rows("Y", Y, rows * N, d, (2,)),
-                                     _rows("Yf32", Yf32, rows * N, d, (4,))), stream)
+    _launch("osc_gemv_grouped", d, stream,
+            (_at("X", X, 2 * Mx * K, d), rows, fan, _at("expert", expert, 4 * rows, d), E, K, G,
+             *_weight_at(E, K, G, L, K_L, QW, SW, WL, N, d), N, _at("Y", Y, 2 * rows * N, d),
+             _at("Yf32", Yf32, 4 * rows * N, d)))
 
 
 def osc_selftest_timeout(limit_us: int = 10000, stream=None):
