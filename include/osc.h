@@ -328,11 +328,12 @@ OSC_API int osc_linear_grouped(const uint8_t* QX, const uint8_t* SX, const uint1
  * top-k for the gate and up projection (X one row per token, expert the tokens' choices in
  * order), 1 for the down projection (X one row per choice). expert: `rows` ids on the DEVICE, in
  * any order and with any repetition, read by the kernel, so a decoding step needs no plan on the
- * host and no sorting; each chosen expert's weight is read once for every 8 or 16 of its rows. An
+ * host and no sorting; each chosen expert's weight is read once for every 8 of its rows. An
  * id < 0 marks an unused row: its Y is zeros. An id >= E is recorded in the status word
  * (OSC_ERR_TABLE) and its row is zeros too. X: (rows + fan - 1) / fan x K; L, QW, SW, WL per expert
  * as in osc_quantize_grouped and osc_linear_grouped (L may be NULL when K_L == 0). Y: rows x N bf16;
- * Yf32 (rows x N) may be NULL. rows and E at most 4096 each: for more rows use osc_linear_grouped. */
+ * Yf32 (rows x N) may be NULL. rows and E at most 4096 each, K at most 32768, E x N below 2^31: for more
+ * rows use osc_linear_grouped. */
 OSC_API int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, int E, int K, int G,
                              const int8_t* L, int R, int K_L, const uint8_t* QW, const uint8_t* SW,
                              const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);

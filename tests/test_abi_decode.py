@@ -99,6 +99,9 @@ def test_row_limits(lib, p16):
     for k in (dict(E=0), dict(E=4097), dict(fan=0), dict(expert=None)):
         assert _grouped(lib, p16, **k) == -1, k
     assert _grouped(lib, p16, expert=_off(p16)) == -2
+    assert _gemv(lib, p16, K=262144 + 256, L=None, K_L=0) == -1
+    assert _grouped(lib, p16, K=32768 + 256, G=64) == -1
+    assert _grouped(lib, p16, E=4096, N=2**19) == -1           # E x N past 31 bits
 
 
 def _cpu(*shape, dtype=torch.bfloat16):

@@ -10,12 +10,15 @@ bf16 half step (2^-8) more of h, Y of y, and a code's value within half a step o
 (2^-4 relative, 2^-10 of the scale near zero) of y cut at 448 of the scale. The exponent follows
 from the largest |y| unless that lies within DY of a power of two.
 
-Products. With A = sum |x| |w| over everything an output sums, each mma adds 17 terms with an error of at most
-17 * 2^-24 of their magnitudes (truncated alignment), in chains of two; at most 4 + 16 + 8 + 8 fp32
-additions (blocks, chunks of a warp up to K = 16384, warps, cluster) and the chain of W_L's mma's
-(17 u each, up to 2 * 24 of them) follow on partial sums below A. Token values below 2^-31 of their run's maximum add at
-most 2^-39 of it each. All together below (34 + 40 + 17 * 48 * 0.06) u A < 150 u A for the
-shares of W_L here (its magnitudes are at most 6 % of A's chain); 200 u A is used. The bf16 output equals the fp32 one rounded."""
+Products. With A = sum |x| |w| over everything an output sums: each mma adds 17 terms with an error of at
+most 17 u of the largest (truncated alignment). They run in chains of eight over four scale blocks (up to 2
+rows), four over two (up to 4 rows) or two over one, so a chain errs by at most 8 * 17 u = 136 u of
+its own share of A and all chains by 136 u A. The fp32 additions that follow err by u A each at most: 4 over
+an item's steps (16 with one scale block of 16 a step, whose chains are single mma's), 20 over a warp's items
+for K up to 16384, 16 over the warps, 8 over a cluster. W_L's mma's run in one chain, up to 48 of 17 u each,
+on at most 6 % of A here: 49 u A. Token values below 2^-31 of their run's maximum add at most 2^-39 of it
+each. Together below (136 + 4 + 20 + 16 + 8 + 49 + 1) u A < 240 u A, which is used. The bf16 output equals the
+fp32 one rounded."""
 import numpy as np
 import pytest
 import torch
@@ -227,7 +230,7 @@ def _x(M, K, seed, scale=1.0):
     return X.bfloat16()
 
 
-def _close(Y, Yf, X64, W64, n_terms=200):
+def _close(Y, Yf, X64, W64, n_terms=240):
     ref = X64 @ W64.t()
     A = X64.abs() @ W64.abs().t()
     off = (Yf.double() - ref).abs()
@@ -267,10 +270,28 @@ def test_gemv_shapes(osc, N, K, M, G):
     X = _x(M, K, N)
     if K <= 16384:
         _run_gemv(osc, w, X)
-    else:                                        # 33 chunks a warp: 17 more additions
+    else:                                        # up to 17 more additions: a warp's items
         Y, Yf = torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), torch.empty((M, N), device="cuda")
         osc.osc_gemv(X, G, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], N, Y, Yf)
-        _close(Y, Yf, X.double(), w["W64"][0], 217)
+        _close(Y, Yf, X.double(), w["W64"][0], 257)
+
+
+@pytest.mark.parametrize("M,K,G", [(1, 262144, 32), (3, 262144, 64), (9, 131072, 16), (16, 16384, 16), (17, 65536, 32)])
+def test_gemv_longest_k(osc, M, K, G):
+    """K in parts over a cluster, fewer tokens a pass where they do not fit. Up to 64 more additions (a
+    warp's items)."""
+    N = 32
+    W = (torch.randn((N, K), generator=_gen(71), device="cuda") * 0.02).bfloat16()
+    QW, SW, _ = osc.prepare_weight(W, G)
+    V = 16 if G == 16 else 32
+    offs = torch.from_numpy(scale_offsets(N, K, V)).cuda()
+    codes = torch.stack((QW & 15, QW >> 4), 2).view(N, K).long()
+    W64 = torch.from_numpy(E2M1).cuda()[codes] * torch.pow(2.0, SW[offs].double() - 127).repeat_interleave(V, 1)
+    X = _x(M, K, 72)
+    Y, Yf = torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), torch.empty((M, N), device="cuda")
+    osc.osc_gemv(X, G, None, 0, QW, SW, None, N, Y, Yf)
+    _close(Y, Yf, X.double(), W64, 304)
+    assert osc.osc_status() == (0, 0)
 
 
 def test_gemv_wide_w_l_and_extremes(osc):
@@ -360,6 +381,29 @@ def test_grouped_id_patterns(osc, rows):
     assert osc.osc_status() == (0, 0)
 
 
+@pytest.mark.parametrize("E,N,K,rows", [(4096, 16, 256, 4096), (2, 16, 32768, 40), (3, 32, 20480, 9), (600, 48, 512, 90)])
+def test_grouped_limits(osc, E, N, K, rows):
+    """The most experts and rows, the longest K (64 more additions there), more experts than threads."""
+    g = _gen(E + K)
+    W = (torch.randn((E, N, K), generator=g, device="cuda") * 0.02).bfloat16()
+    QW = torch.empty((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    SW = torch.empty((E, 128 * K // 32), dtype=torch.uint8, device="cuda")
+    for e in range(E):
+        QW[e], SW[e], _ = osc.prepare_weight(W[e], 32)
+    ids = torch.randint(0, E, (rows,), generator=g, device="cuda").to(torch.int32)
+    X = _x(rows, K, 5)
+    Y, Yf = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda"), torch.empty((rows, N), device="cuda")
+    osc.osc_gemv_grouped(X, 1, ids, E, 32, None, 0, QW, SW, None, N, Y, Yf)
+    offs = torch.from_numpy(scale_offsets(N, K, 32)).cuda()
+    val = torch.from_numpy(E2M1).cuda()
+    for r in range(0, rows, max(1, rows // 64)):
+        q = QW[int(ids[r])]
+        w = val[torch.stack((q & 15, q >> 4), 2).view(N, K).long()]
+        w = w * torch.pow(2.0, SW[int(ids[r])][offs].double() - 127).repeat_interleave(32, 1)
+        _close(Y[r:r + 1], Yf[r:r + 1], X[r:r + 1].double(), w, 304)
+    assert osc.osc_status() == (0, 0)
+
+
 def test_grouped_id_out_of_range_is_reported(osc):
     w = _layer(osc, 5, 128, 512, 32, 1, 0.7, 41)
     ids = torch.tensor([0, 5, 4, 2**31 - 1, -2**31, 4], dtype=torch.int32, device="cuda")
@@ -431,11 +475,11 @@ def _check_step(s, M=3):
     # each product against its own input as it was rounded (bf16 rows, 8-bit codes), in 64 bits
     ref = s["y"].double() @ s["qkv"]["W64"][0].t()
     A = s["y"].double().abs() @ s["qkv"]["W64"][0].abs().t()
-    assert bool(((s["z"].double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 201 * U * A).all())
+    assert bool(((s["z"].double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 241 * U * A).all())
     for r, e in enumerate(s["ids"].tolist()):
         x = s["y"][r // 2].double()
         ref, A = s["up"]["W64"][e] @ x, s["up"]["W64"][e].abs() @ x.abs()
-        assert bool(((s["u"][r].double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 201 * U * A).all())
+        assert bool(((s["u"][r].double() - ref).abs() <= ref.abs() * 2.0 ** -8 + 241 * U * A).all())
     # and the FP8 module against the unquantized product: half a step of E4M3 on either side,
     # 2^-4 relative each (or 2^-10 of a scale that is at most 2^-8 of the block's maximum: the
     # small values' share, below 2^-10 of the block), the product of both, and bf16

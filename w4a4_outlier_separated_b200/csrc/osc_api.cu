@@ -713,7 +713,7 @@ int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int
   if (M == 0 && N > 0 && K > 0 && K_L >= 0) return OSC_OK;  // nothing to read or write
   int rc = check_gemv(X, M, K, G, L, R, K_L, QW, SW, WL, N, Y, Yf32);
   if (rc != OSC_OK) return rc;
-  if (M > 65535 * 16) return OSC_ERR_ARG;
+  if (M > 65535 * 16 || K > osc::GEMV_MAX_K) return OSC_ERR_ARG;
   DeviceState* ds = nullptr;
   if ((rc = device_state(&ds)) != OSC_OK) return rc;
   osc::GemvParams p{X, M, N, K, G, L, R, K_L, QW, SW, WL, Y, Yf32, ds->status, nullptr, 1, 1};
@@ -728,7 +728,8 @@ int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, in
   if (rows == 0 && N > 0 && K > 0 && K_L >= 0) return OSC_OK;  // nothing to read or write
   int rc = check_gemv(X, rows, K, G, L, R, K_L, QW, SW, WL, N, Y, Yf32);
   if (rc != OSC_OK) return rc;
-  if (!expert || rows > osc::GEMV_MAX_ROWS) return OSC_ERR_ARG;
+  if (!expert || rows > osc::GEMV_MAX_ROWS || K > osc::GEMV_GROUPED_MAX_K) return OSC_ERR_ARG;
+  if ((long long)E * N >= (1LL << 31)) return OSC_ERR_ARG;
   if (!a16(expert)) return OSC_ERR_ALIGN;
   DeviceState* ds = nullptr;
   if ((rc = device_state(&ds)) != OSC_OK) return rc;

@@ -866,8 +866,9 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaSt
   return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED, TWO>, maps, p);
 }
 
-// The split of one call. CH, NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Returns
-// cudaErrorInvalidValue, and launches nothing, where `try_only` and the tokens of a pass would not fit one CTA.
+// The split of one call. CH, NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Where `try_only` and
+// the tokens of a pass would not fit one CTA it returns cudaErrorInvalidValue and launches nothing; else it
+// splits K further, then takes fewer tokens a pass (one always fits within the limits of the entry points).
 template <int CH, int NT, int NW, int ST, bool GROUPED, bool TWO = false>
 cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int V = p.G == 16 ? 16 : 32;
@@ -879,7 +880,8 @@ cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   };
   // parts of K: to fill the SMs where units are few, and for the tokens to fit
   const int max_s = GROUPED ? 1 : 8;
-  p.S = std::max(1, std::min({max_s, num_sms / std::max(1, p.n_units * ((p.M + p.mt - 1) / p.mt)), chunks / NW}));
+  const long long units = std::max<long long>(1, (long long)p.n_units * ((p.M + p.mt - 1) / p.mt));
+  p.S = std::max(1, std::min({max_s, (int)(num_sms / units), chunks / NW}));
   while (smem_of(p.S) > GV_SMEM_MAX) {
     if (try_only) return cudaErrorInvalidValue;
     if (p.S < max_s && chunks / (p.S + 1) >= NW) ++p.S;
@@ -911,7 +913,8 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   p.rows32 = p.N % 32 == 0;
   if (p.expert) {
     p.mt = std::min(p.M, 8);
-    return launch_v<256, 1, 16, 2, true>(p, false, num_sms, s);
+    const cudaError_t e = launch_v<256, 1, 16, 2, true>(p, true, num_sms, s);
+    return e != cudaErrorInvalidValue ? e : launch_v<256, 1, 8, 2, true>(p, false, num_sms, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;

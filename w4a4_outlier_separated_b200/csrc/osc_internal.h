@@ -101,7 +101,8 @@ struct GemvParams {
   int* status;
   const int* expert;       // grouped: M expert ids (device); nullptr = dense
   int fan, E;              // grouped: row r reads X row r / fan
-  // set by the launcher
+  // set by the launcher: parts of K, CTAs per part, 32-row units, most tokens of a pass, channels and 256-channel
+  // items of a part, log2 G, whether N is a multiple of 32
   int S, n_cta, n_units, mt, kc, nc_base, nc_more, g_shift, rows32;
   long long w_each, w_more;   // units of each CTA, CTAs with one more (dense)
 };
@@ -114,6 +115,9 @@ cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const v
 // grouped form: most rows and experts of one call (their ids are staged in shared memory)
 constexpr int GEMV_MAX_ROWS = 4096;
 constexpr int GEMV_MAX_EXPERTS = 4096;
+// longest K: one token of a CTA's part fits in shared memory beside the weight ring (dense: K in up to 8 parts)
+constexpr int GEMV_MAX_K = 262144;
+constexpr int GEMV_GROUPED_MAX_K = 32768;
 cudaError_t launch_gemv(const GemvParams& p, int num_sms, cudaStream_t s);
 
 struct GroupedQuantParams {
