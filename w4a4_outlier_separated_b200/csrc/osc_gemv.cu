@@ -5,9 +5,9 @@
 //
 // Unit: 32 weight rows, the four octets {q*32 + j*8 .. +7} (q = 0..3) of a 128-row block, because
 // the scale layout keeps exactly those rows' words together: 128 contiguous bytes per 512-byte
-// atom. Item: a unit's codes and scales of CH channels, or its W_L of CH / 4 columns (both CH / 2
-// bytes a row). The work is the units of every pass (an expert's rows, mt at a time; the dense form
-// is one expert), in one line; each CTA takes an equal run of it, whose parts of one pass are its
+// atom. Item: a unit's codes and scales of 256 channels, or its W_L of 64 columns (both 128 bytes a
+// row). The work is the units of every pass (an expert's rows, mt at a time; the dense form is one
+// expert), in one line; each CTA, one per SM, takes an equal run of it, whose parts of one pass are its
 // segments. A segment stages its tokens once; teams of warps share its units, a team's warps a
 // unit's items. Each warp copies its items by TMA into its own ring of stages, running ahead over the
 // ends of units, and computes without waiting for another warp; a unit's sums meet in shared memory
@@ -16,13 +16,26 @@
 //
 // Arithmetic: mma.m16n8k16 on f16 operands with fp32 accumulators, the weight rows as the
 // 16-row side and the tokens as the 8-wide side. E2M1 codes become f16 exactly (one conversion
-// per two codes). The bf16 tokens become f16 after scaling each token's 128 channels by the power
+// per two codes). The bf16 tokens become f16 after scaling each token's 256 channels by the power
 // of two that puts their largest magnitude in [2^14, 2^15): a value keeps all its bits down to
 // 2^-31 of that maximum, and below that errs by at most 2^-39 of it, far under the fp32 sum's own
 // rounding. A scale block's products are summed in fp32, then multiplied by the weight's and the
 // token's powers of two (exact) and added in fp32. Y is rounded once.
+// With one or two tokens an mma takes four scale blocks at once, each in columns of its own (two with up to
+// four tokens): a quarter of the scalings and of the shared-memory reads.
 // The protected channels are zeroed in the staged tokens and kept apart in bf16; their products
 // with W_L run as bf16 mma into the same sums.
+//
+// Measured (B200, launches back to back in a graph, weights cold): K = 4096, one token, N = 98304 (201 MB):
+// 37.8 us, 5.3 TB/s, 86 % of the copy bandwidth. N = 24576: 13.7 us against a floor of 8.5; N = 6144: 7.0 us
+// against 2.2. What is left there is the start, about 5000 cycles before the first item is multiplied
+// (the tokens' and the table's round trip, their conversion by every CTA), and 1.3 or 5.2 units to an SM. In
+// the stream itself the ALU pipe (two cycles a conversion) and the memory are about even: 460 cycles per
+// item and SM sub-partition. With 9 to 16 tokens the conversion of the tokens takes 5 of 26 us (N = 24576)
+// and the mma's as long as the memory. Measured slower: one warp's ring filled with cp.async instead of TMA
+// (FFN 19 against 17 us at the time), one team of 16 warps per unit (20 against 16.4 us), sums handed over
+// through mbarriers without any team barrier (QKV 7.7 against 7.0 us), two CTAs of 8 warps per SM (same time,
+// 4 rows 19.1 against 16.5 us).
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -34,10 +47,10 @@ namespace osc {
 namespace {
 
 constexpr int GV_ROWS = 32;                       // weight rows of a unit
+constexpr int CH = 256;                           // channels of an item: 128 bytes of codes a row
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 // Arrive on an mbarrier when this thread's earlier cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -138,15 +151,15 @@ __device__ __forceinline__ int cluster_id() {
   return (int)r;
 }
 
-// Shared memory of a CTA, in bytes from its start. CH: channels of an item; kc: channels of this
-// CTA's K range (at most); cols: W_L columns.
+// Shared memory of a CTA, in bytes from its start. kc: channels of this CTA's K range (at most); cols: W_L
+// columns.
 struct GvSmem {
   int stage, warp, sc, x, zero, red, xs, b, bcols, ent, ids, cnt, at, total;
 };
 // A warp's sums: row r of token m at m * 32 + (r ^ (m / 2 % 4) * 8), so that the mma fragments' stores
 // (tokens 2t, rows g) and the reads (4 rows a lane) meet different banks.
 __host__ __device__ constexpr int gv_sums(int NT) { return 8 * NT * GV_ROWS * 4; }
-__host__ __device__ inline GvSmem gv_smem(int V, int CH, int NT, int NW, int ST, int mt, int kc, int cols, int n_table,
+__host__ __device__ inline GvSmem gv_smem(int V, int NT, int NW, int ST, int mt, int kc, int cols, int n_table,
                                           int rows, int E) {
   GvSmem m;
   m.stage = GV_ROWS * CH / 2;                                      // codes, or W_L columns
@@ -174,9 +187,9 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 }  // namespace
 
-// V: channels of a scale slot; CH: channels of an item; NT: token tiles of 8; NW: warps; ST: stages per warp; TWO: the
+// V: channels of a scale slot; NT: token tiles of 8; NW: warps; ST: stages per warp; TWO: the
 // passes have one or two tokens.
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED, bool TWO>
+template <int V, int NT, int NW, int ST, bool GROUPED, bool TWO>
 __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -193,14 +206,14 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   constexpr int RB = CH / 2;                               // bytes of an item's row: codes, or CH / 4 W_L columns
   constexpr int COLS = CH / 4;
   constexpr int SBYTES = GV_ROWS * CH / V;                 // scales of an item
-  constexpr int XB = CH / 16;                              // bytes of a lane when an item's tokens are copied
+  constexpr int XB = CH / 16;                              // bytes of a lane of an item of a token
   static_assert(NT == 1 || gv_sums(NT) <= GV_ROWS * RB, "a stage takes a warp's sums");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S;
   const int cta = S == 1 ? blockIdx.x : cluster_id(), rank = S == 1 ? 0 : cluster_ctarank();
   const int N = p.N, K = p.K;
   const int n_table = p.L ? (K >> p.g_shift) * p.R : 0;
-  const GvSmem sm = gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
+  const GvSmem sm = gv_smem(V, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
   const uint32_t sbase = smem_u32(smem);
   const int swarp = warp * sm.warp, sscale = sm.sc + warp * (ST * SBYTES);
   auto ld32 = [&](int off) { return *reinterpret_cast<const uint32_t*>(smem + off); };
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         }
       }
       if (pj < nc && lane * 16 < SBYTES)
-        cp_async<16>(sbase + sscale + to * SBYTES + lane * 16,
+        cp_async16(sbase + sscale + to * SBYTES + lane * 16,
                      sfrom + ((size_t)(pu >> 2) * satoms + (size_t)pj * (CH / V / 4)) * 512 + (pu & 3) * 128);
       cp_async_arrive(bars + to * 8);
       pj += tw;
@@ -489,13 +502,8 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           for (int y = 0; y < MB; ++y) {
             const int m = MB == 1 ? m0 : min(m0 + y, nt_rows - 1);
             const uint8_t* const x = xc + m * p.kc * 2 + lane * XB;
-            if constexpr (XB == 8) {
-              const uint2 q = *reinterpret_cast<const uint2*>(x);
-              v[y][0] = q.x; v[y][1] = q.y;
-            } else {
-              const uint4 q = *reinterpret_cast<const uint4*>(x);
-              v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
-            }
+            const uint4 q = *reinterpret_cast<const uint4*>(x);
+            v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
           }
           if (n_table)
             for (int r = 0; r < p.R; ++r) {
@@ -520,8 +528,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           __syncwarp();
 #pragma unroll
           for (int y = 0; y < MB; ++y) {
-            uint32_t a = maxabs2(v[y][0], v[y][1]);
-            if constexpr (XB == 16) a = maxabs2(a, maxabs2(v[y][2], v[y][3]));
+            const uint32_t a = maxabs2(maxabs2(v[y][0], v[y][1]), maxabs2(v[y][2], v[y][3]));
             am[y] = max(a & 0x7FFFu, (a >> 16) & 0x7FFFu);
           }
 #pragma unroll
@@ -535,8 +542,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
             for (int i = 0; i < XB / 4; ++i)
               v[y][i] = pack_f16x2(__uint_as_float(v[y][i] << 16) * f, __uint_as_float(v[y][i] & 0xFFFF0000u) * f);
             uint8_t* const x = xc + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6));
-            if constexpr (XB == 8) *reinterpret_cast<uint2*>(x) = make_uint2(v[y][0], v[y][1]);
-            else *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
+            *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
             if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
           }
         }
@@ -561,8 +567,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       constexpr int STEP = V * P;                          // channels of a step
       constexpr int LB = STEP / 8;                         // a lane's code bytes of a step and row
       const int rg = (g & 1) << 2 | (g & 2) | g >> 2;
-      const int rsw = CH == 256 ? rg : (rg >> 1) & 3;      // swizzle of the lane's row in each octet
-      const int rd = rg * RB + (((t * LB >> 4) ^ rsw) << 4) + (t * LB & 15), rw = rg * RB + ((t ^ rsw) << 4);   // codes, W_L
+      const int rd = rg * RB + (((t * LB >> 4) ^ rg) << 4) + (t * LB & 15), rw = rg * RB + ((t ^ rg) << 4);   // codes, W_L
       int xa[NT], ba[NT];
       bool live[NT];
 #pragma unroll
@@ -822,11 +827,11 @@ namespace {
 
 // Tensor maps of the codes and of W_L, one copy of an item each. Rows as (32 rows) x (blocks of 32), so
 // that one box {a row's bytes, 8 rows, 4 blocks} is a unit's four octets; where N is not a multiple of
-// 32 as one run of rows, a box of 8. Swizzled by the row length, so that 8 rows' equal pieces meet
+// 32 as one run of rows, a box of 8. Swizzled by the 128-byte row, so that 8 rows' equal pieces meet
 // different banks.
-cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int CH, int E) {
+cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int E) {
   const uint64_t rows = (uint64_t)E * p.N;
-  const CUtensorMapSwizzle sw = CH == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   auto operand = [&](CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t width, uint64_t pitch, uint32_t box) {
     const uint64_t d3[3] = {width, 32, rows / 32}, s3[2] = {pitch, pitch * 32};
     const uint64_t d1[3] = {width, rows, 1}, s1[2] = {pitch, pitch * rows};
@@ -841,11 +846,11 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int CH, int E) {
 
 constexpr int GV_SMEM_MAX = 232448 - 8192;                 // 227 KB less the static part and a reserve
 
-template <int V, int CH, int NT, int NW, int ST, bool GROUPED, bool TWO>
+template <int V, int NT, int NW, int ST, bool GROUPED, bool TWO>
 cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaStream_t s) {
   static PerDeviceOnce attr_once;
   const cudaError_t ae = attr_once.run([] {
-    return cudaFuncSetAttribute(gemv_kernel<V, CH, NT, NW, ST, GROUPED, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(gemv_kernel<V, NT, NW, ST, GROUPED, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 GV_SMEM_MAX);
   });
   if (ae != cudaSuccess) return ae;
@@ -863,20 +868,20 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaSt
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, CH, NT, NW, ST, GROUPED, TWO>, maps, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<V, NT, NW, ST, GROUPED, TWO>, maps, p);
 }
 
-// The split of one call. CH, NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Where `try_only` and
+// The split of one call. NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Where `try_only` and
 // the tokens of a pass would not fit one CTA it returns cudaErrorInvalidValue and launches nothing; else it
 // splits K further, then takes fewer tokens a pass (one always fits within the limits of the entry points).
-template <int CH, int NT, int NW, int ST, bool GROUPED, bool TWO = false>
+template <int NT, int NW, int ST, bool GROUPED, bool TWO = false>
 cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int V = p.G == 16 ? 16 : 32;
   const int chunks = p.K / CH;
   const int n_table = p.L ? p.K / p.G * p.R : 0;
   auto smem_of = [&](int S) {
     p.kc = (chunks + S - 1) / S * CH;
-    return gv_smem(V, CH, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
+    return gv_smem(V, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
   };
   // parts of K: to fill the SMs where units are few, and for the tokens to fit
   const int max_s = GROUPED ? 1 : 8;
@@ -898,14 +903,21 @@ cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   p.w_each = work / p.n_cta;
   p.w_more = work % p.n_cta;
   GemvMaps maps;
-  const cudaError_t e = encode_gemv_maps(&maps, p, CH, GROUPED ? p.E : 1);
+  const cudaError_t e = encode_gemv_maps(&maps, p, GROUPED ? p.E : 1);
   if (e != cudaSuccess) return e;
-  return V == 16 ? launch_t<16, CH, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s)
-                 : launch_t<32, CH, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s);
+  return V == 16 ? launch_t<16, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s)
+                 : launch_t<32, NT, NW, ST, GROUPED, TWO>(maps, p, smem, s);
 }
 
 }  // namespace
 
+// The variant by the rows alone, and by what fits:
+//   1 .. 8 rows and routed rows: one token tile, 16 warps with two stages each. One or two rows have a kernel of their
+//   own, without the code for more (N = 6144: 7.1 against 7.4 us). Where the tokens and tables leave too little room for
+//   that ring: 8 warps (8 rows of K = 4096: 19.5 us, against 31 us for 16 warps on a K split in two).
+//   9 rows and more: two token tiles, 16 rows a pass, 8 warps with the registers of 16 (16 rows, N = 24576: 26.1 us,
+//   against 30.2 us in passes of 8 rows and 31.5 us with 16 warps on items of 128 channels).
+// K is split where the units alone would leave SMs idle (one row, K = 12288, N = 1024: 5.4 against 8.0 us).
 cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   GemvParams p = q;
   p.n_units = p.N / 128 * 4 + std::min(4, p.N % 128 / 8);
@@ -913,17 +925,17 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   p.rows32 = p.N % 32 == 0;
   if (p.expert) {
     p.mt = std::min(p.M, 8);
-    const cudaError_t e = launch_v<256, 1, 16, 2, true>(p, true, num_sms, s);
-    return e != cudaErrorInvalidValue ? e : launch_v<256, 1, 8, 2, true>(p, false, num_sms, s);
+    const cudaError_t e = launch_v<1, 16, 2, true>(p, true, num_sms, s);
+    return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 2, true>(p, false, num_sms, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    const cudaError_t e = p.M <= 2 ? launch_v<256, 1, 16, 2, false, true>(p, true, num_sms, s)
-                                   : launch_v<256, 1, 16, 2, false>(p, true, num_sms, s);
-    return e != cudaErrorInvalidValue ? e : launch_v<256, 1, 8, 3, false>(p, false, num_sms, s);
+    const cudaError_t e = p.M <= 2 ? launch_v<1, 16, 2, false, true>(p, true, num_sms, s)
+                                   : launch_v<1, 16, 2, false>(p, true, num_sms, s);
+    return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 3, false>(p, false, num_sms, s);
   }
   p.mt = std::min(p.M, 16);
-  return launch_v<256, 2, 8, 2, false>(p, false, num_sms, s);
+  return launch_v<2, 8, 2, false>(p, false, num_sms, s);
 }
 
 }  // namespace osc

@@ -12,7 +12,14 @@
 //
 // Work split: 8 consecutive channels per thread and step (one 16-byte load of each input, one
 // 8-byte store of codes), four neighbouring threads to a 32-channel block, whole warps to a
-// row, so that the block maximum meets by shuffles.
+// row, so that the block maximum meets by shuffles. One CTA per row (or a few short rows): a row's sum
+// needs all of it, so what keeps the memory busy is the other rows' CTAs on the SM.
+//
+// Measured (B200, launches back to back in a graph, inputs cold): 16384 x 4096 with a residual 74.2 us, 6.3 TB/s, 96 % of
+// the copy bandwidth. 2048 x 4096: 12.0 us against 9.0 (the fill and the drain of 14 rows per SM). 4001 x 6144
+// without a residual: 19.8 us against 11.4; there 545 instructions per 1024 channels bind before the memory. One
+// row: 2.0 us, the launch. Measured slower: persistent CTAs with the next row's loads in registers (4001 x 6144: 23.7
+// us) or with a ring of rows in shared memory (31 us): fewer rows are worked on at once.
 #include "osc_device.cuh"
 #include "osc_internal.h"
 
@@ -214,6 +221,8 @@ static cudaError_t launch_c(const AddNormParams& p, int tpr, cudaStream_t s) {
 }
 
 cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s) {
+  // steps per thread: one where rows are few, so that a row has the most threads (one row of 4096: 2.0 against 2.6 us with
+  // four steps), four where they fill the SMs (2048 rows: 12.1 against 13.2 us, 16384 rows: 74 against 90 us)
   const int nchunk = p.K / 8;
   auto tpr = [&](int c) { return ((nchunk + c - 1) / c + 31) / 32 * 32; };
   int c = p.M >= 4 * num_sms ? 4 : 1;

@@ -14,6 +14,9 @@ CASE:
   w2_fp8        osc_quantize_fp8 + osc_linear_fp8_fallback on the down projection
   moe_gateup    osc_quantize_grouped + osc_linear_grouped, 128 experts, 2048 -> 1536
   moe_down      the same for the expert down projection, 768 -> 2048
+  norm_fp8      osc_add_rmsnorm_quantize_fp8, K=4096, M=--m (2048), with a residual
+  gemv          osc_gemv, FFN up weights (K=4096, N=24576), M=--m (1), G=--g
+  gemv_moe      osc_gemv_grouped, --m tokens (1) through 8 of 128 experts, 2048 -> 1536, random codes
 
 Inputs are the seeded synthetic workloads of inputs.py; tables come from osc_build_table on
 the GPU and weights from osc_prepare_weight (or osc_quantize_fp8), so the set-up launches come
@@ -116,12 +119,43 @@ def _moe(which, launches):
         osc.osc_linear_grouped(QX, SX, B, QW, SW, WL, mbed, kld, E, Mp, N, K, G, K_L, Y)
 
 
+def _norm_fp8(M, K, launches):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X, res = (torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    H = torch.empty_like(X)
+    QX, SX, _ = osc.alloc_quantize_outputs(M, K, 32, 0, fp8=True)
+    for _ in range(launches):
+        osc.osc_add_rmsnorm_quantize_fp8(X, res, gamma, 1e-6, H, None, QX, SX)
+
+
+def _gemv(case, G, M, launches):
+    X = _dev(case.X[:M])
+    N, K = case.W.shape
+    Ld, K_L = _table(case.calib, K, G)
+    QW, SW, WL = osc.prepare_weight(_dev(case.W), G, Ld, K_L)
+    Y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    for _ in range(launches):
+        osc.osc_gemv(X, G, Ld, K_L, QW, SW, WL, N, Y)
+
+
+def _gemv_moe(T, launches, E=128, K=2048, N=1536, top=8):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn((T, K), generator=gen, device="cuda").to(torch.bfloat16)
+    QW = torch.randint(0, 256, (E, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    SW = torch.full((E, osc.osc_scale_bytes(N, K, 32)), 120, dtype=torch.uint8, device="cuda")
+    ids = torch.rand((T, E), generator=gen, device="cuda").topk(top, 1).indices.reshape(-1).to(torch.int32)
+    Y = torch.empty((T * top, N), dtype=torch.bfloat16, device="cuda")
+    for _ in range(launches):
+        osc.osc_gemv_grouped(X, top, ids, E, 32, None, 0, QW, SW, None, N, Y)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("case", choices=["qkv", "qkv_rmsnorm", "weight_bound", "weight_bound_split", "ffn", "w2_osc",
-                                     "w2_fp8", "moe_gateup", "moe_down"])
+                                     "w2_fp8", "moe_gateup", "moe_down", "norm_fp8", "gemv", "gemv_moe"])
     ap.add_argument("--launches", type=int, default=4, help="rounds of the workload's kernels")
-    ap.add_argument("--m", type=int, default=None, help="token rows (qkv: 2048, weight_bound: 16)")
+    ap.add_argument("--m", type=int, default=None, help="token rows (qkv, norm_fp8: 2048, weight_bound: 16, gemv, gemv_moe: 1)")
     ap.add_argument("--g", type=int, default=32, help="group size (qkv, ffn)")
     a = ap.parse_args(argv)
     osc.lib()
@@ -137,6 +171,12 @@ def main(argv=None):
         _dense(I.w2_case(), 32, a.launches)
     elif a.case == "w2_fp8":
         _fp8(I.w2_case(), a.launches)
+    elif a.case == "norm_fp8":
+        _norm_fp8(a.m or 2048, 4096, a.launches)
+    elif a.case == "gemv":
+        _gemv(I.ffn_case(a.g), a.g, a.m or 1, a.launches)
+    elif a.case == "gemv_moe":
+        _gemv_moe(a.m or 1, a.launches)
     else:
         _moe(a.case[4:], a.launches)
     torch.cuda.synchronize()
