@@ -87,10 +87,11 @@ __device__ __forceinline__ uint32_t e4m3x4(f2 a, f2 b) {
   return r;
 }
 
-// What follows the sum of squares of a row, for the calling thread's 8 channels of step `ch`: the normed values,
-// their block's exponent, the codes and (one lane in four) the scale. A warp's lanes hold consecutive steps.
-__device__ __forceinline__ void norm_quant8(const AddNormParams& p, size_t base, uint8_t* srow, int ch, const f2 (&h)[4],
-                                            f2 inv2, const uint4& gamma) {
+// What follows the sum of squares of a row, for 8 channels of the calling thread: the normed values (at yp, where
+// wanted), their block's exponent, the codes (at q) and (one lane in four) the scale. A warp's lanes hold consecutive
+// channels.
+__device__ __forceinline__ void norm_quant8(const f2 (&h)[4], f2 inv2, const uint4& gamma, uint16_t* yp, uint8_t* qp,
+                                            uint8_t* sp) {
   const int lane = threadIdx.x & 31;
   f2 g[4], y[4];
   unpack8(gamma, g);
@@ -102,7 +103,7 @@ __device__ __forceinline__ void norm_quant8(const AddNormParams& p, size_t base,
     unpack2(y[i], lo, hi);
     am = fmaxf(am, fmaxf(fabsf(lo), fabsf(hi)));
   }
-  if (p.Y) *reinterpret_cast<uint4*>(p.Y + base + (size_t)ch * 8) = pack8(y);
+  if (yp) *reinterpret_cast<uint4*>(yp) = pack8(y);
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
   // the exponent e = floor(log2 amax) - 8, at least -127 (also for a zero or subnormal block), as its byte e + 127
@@ -110,9 +111,9 @@ __device__ __forceinline__ void norm_quant8(const AddNormParams& p, size_t base,
   const float f = __uint_as_float((uint32_t)(254 - byte) << 23);   // 2^-e: the product is exact
   const f2 ff = pack2(f, f);
   const uint2 q = make_uint2(e4m3x4(mul2f(y[0], ff), mul2f(y[1], ff)), e4m3x4(mul2f(y[2], ff), mul2f(y[3], ff)));
-  *reinterpret_cast<uint2*>(p.Q + base + (size_t)ch * 8) = q;
+  *reinterpret_cast<uint2*>(qp) = q;
   // one byte of each four lanes; a layout word's four bytes meet in one write of the warp
-  if ((lane & 3) == 0) srow[(size_t)(ch >> 4) * 512 + ((ch >> 2) & 3)] = (uint8_t)byte;
+  if ((lane & 3) == 0) *sp = (uint8_t)byte;
 }
 
 // The first scale word of a row (the next ones 512 bytes apart): atoms of 128 rows x 4 slots.
@@ -129,9 +130,9 @@ __device__ __forceinline__ f2 inverse2(const AddNormParams& p, float ss) {
 
 }  // namespace
 
-// C: steps of 8 channels per thread; RES: there is a residual. A CTA holds p.rows_per_cta rows of `tpr`
-// threads each. Rows M .. (next multiple of 128) only write zero scales.
-template <int C, bool RES>
+// C: steps of 8 channels per thread; RES: there is a residual; WHOLE: every thread has all its steps. A CTA holds
+// p.rows_per_cta rows of `tpr` threads each. Rows M .. (next multiple of 128) only write zero scales.
+template <int C, bool RES, bool WHOLE>
 __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, int tpr) {
   __shared__ float part[32];
   const int sub = threadIdx.x / tpr, t = threadIdx.x - sub * tpr;
@@ -139,8 +140,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
   const int row = blockIdx.x * p.rows_per_cta + sub;
   const int nchunk = p.K >> 3;
   const bool live = row < p.M;
-  const size_t base = (size_t)row * p.K;
-  uint8_t* const srow = scale_row(p, row);
+  const size_t first = (size_t)row * p.K + t * 8;        // the thread's first channel; its steps are tpr * 8 apart
+  uint8_t* srow = scale_row(p, row) + (size_t)(t >> 4) * 512 + ((t >> 2) & 3);
 
   grid_dep_wait();
   grid_dep_launch();
@@ -148,26 +149,26 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
   f2 ss2 = pack2(0.f, 0.f);
   if (live) {
     uint4 a[C], b[C];
+    const uint16_t *x = p.X + first, *r = p.res + first;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = c * tpr + t;
-      if (ch < nchunk) {
-        a[c] = load_stream(p.X + base + (size_t)ch * 8);
-        if (RES) b[c] = load_stream(p.res + base + (size_t)ch * 8);
+    for (int c = 0; c < C; ++c, x += tpr * 8, r += tpr * 8) {
+      if (WHOLE || c * tpr + t < nchunk) {
+        a[c] = load_stream(x);
+        if (RES) b[c] = load_stream(r);
       }
     }
+    uint16_t* hp = p.H + first;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = c * tpr + t;
-      if (ch < nchunk) {
+    for (int c = 0; c < C; ++c, hp += tpr * 8) {
+      if (WHOLE || c * tpr + t < nchunk) {
         unpack8(a[c], h[c]);
         if (RES) {
-          f2 r[4];
-          unpack8(b[c], r);
+          f2 v[4];
+          unpack8(b[c], v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[c][i] = add2(h[c][i], r[i]);
+          for (int i = 0; i < 4; ++i) h[c][i] = add2(h[c][i], v[i]);
         }
-        if (p.H) *reinterpret_cast<uint4*>(p.H + base + (size_t)ch * 8) = pack8(h[c]);
+        if (p.H) *reinterpret_cast<uint4*>(hp) = pack8(h[c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss2 = fma2(h[c][i], h[c][i], ss2);
       }
@@ -187,20 +188,26 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_fp8_kernel(AddNormParams p, 
   }
   if (!live) {
     if (row < ((p.M + 127) & ~127))
-      for (int s = t; s < (p.K >> 7); s += tpr) *reinterpret_cast<uint32_t*>(srow + (size_t)s * 512) = 0u;
+      for (int s = t; s < (p.K >> 7); s += tpr) *reinterpret_cast<uint32_t*>(scale_row(p, row) + (size_t)s * 512) = 0u;
     return;
   }
   const f2 inv2 = inverse2(p, ss);
+  const uint16_t* gp = p.gamma + t * 8;
+  uint8_t* q = p.Q + first;
+  uint16_t* y = p.Y ? p.Y + first : nullptr;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int ch = c * tpr + t;
-    if (ch >= nchunk) break;                             // the same for a whole warp
-    norm_quant8(p, base, srow, ch, h[c], inv2, *reinterpret_cast<const uint4*>(p.gamma + (size_t)ch * 8));
+    if (!WHOLE && c * tpr + t >= nchunk) break;          // the same for a whole warp
+    norm_quant8(h[c], inv2, *reinterpret_cast<const uint4*>(gp), y, q, srow);
+    gp += tpr * 8;
+    q += tpr * 8;
+    srow += (size_t)(tpr >> 4) * 512;
+    if (y) y += tpr * 8;
   }
 }
 
-template <int C, bool RES>
-static cudaError_t launch_r(AddNormParams p, int tpr, cudaStream_t s) {
+template <int C, bool RES, bool WHOLE>
+static cudaError_t launch_w(AddNormParams p, int tpr, cudaStream_t s) {
   p.rows_per_cta = std::max(1, 128 / tpr);
   cudaLaunchConfig_t cfg = {};
   const int mpad = (p.M + 127) / 128 * 128;
@@ -212,12 +219,14 @@ static cudaError_t launch_r(AddNormParams p, int tpr, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, add_rmsnorm_fp8_kernel<C, RES>, p, tpr);
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_fp8_kernel<C, RES, WHOLE>, p, tpr);
 }
 
 template <int C>
 static cudaError_t launch_c(const AddNormParams& p, int tpr, cudaStream_t s) {
-  return p.res ? launch_r<C, true>(p, tpr, s) : launch_r<C, false>(p, tpr, s);
+  const bool whole = C * tpr * 8 == p.K;
+  if (p.res) return whole ? launch_w<C, true, true>(p, tpr, s) : launch_w<C, true, false>(p, tpr, s);
+  return whole ? launch_w<C, false, true>(p, tpr, s) : launch_w<C, false, false>(p, tpr, s);
 }
 
 cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s) {
