@@ -272,7 +272,10 @@ OSC_API int osc_linear_fp8_fallback(const uint8_t* QX8, const uint8_t* SX, const
  * is rounded once (unlike osc_rmsnorm_quantize, which quantizes bf16 rows). res (M x K bf16) may
  * be NULL (h = X); H and Y (M x K bf16) may each be NULL (not written). H may be X or res itself
  * (the stream updated in place); otherwise no output may overlap an input or another output.
- * eps >= 0; an all-zero row with eps = 0 gives zeros. fp32 sums: |h| below 1e18. K at most 32768. */
+ * eps >= 0; an all-zero row with eps = 0 gives zeros. The squares are summed in fp32: values up to
+ * 1e17 cannot overflow the sum, and below 1e-18 their squares lose bits, which shows where eps = 0.
+ * A NaN makes its row's codes and Y NaN, an infinity its own code and Y; other rows are not touched.
+ * K at most 32768. */
 OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res, const uint16_t* gamma, float eps,
                                          int M, int K, uint16_t* H, uint16_t* Y, uint8_t* QX8, uint8_t* SX,
                                          osc_stream_t stream);

@@ -165,6 +165,24 @@ def test_norm_edge_rows(osc):
     assert int((Q & 0x7F).count_nonzero()) == 0 and int(S.count_nonzero()) == 0
 
 
+@pytest.mark.parametrize("M,K", [(5, 256), (3, 4096), (700, 512)])
+def test_norm_nan_and_infinity_stay_in_their_rows(osc, M, K):
+    X, res, gamma = _norm_case(M, K, 10)
+    Y, Q = torch.empty((2, M, K), dtype=torch.bfloat16, device="cuda"), torch.empty((2, M, K), dtype=torch.uint8, device="cuda")
+    S = torch.empty((2, (M + 127) // 128 * 128 * K // 32), dtype=torch.uint8, device="cuda")
+    osc.osc_add_rmsnorm_quantize_fp8(X, res, gamma, 1e-6, None, Y[0], Q[0], S[0])
+    X[0, 33] = float("nan")
+    res[2, 7] = float("-inf")
+    osc.osc_add_rmsnorm_quantize_fp8(X, res, gamma, 1e-6, None, Y[1], Q[1], S[1])
+    keep = [i for i in range(M) if i not in (0, 2)]
+    assert torch.equal(Y[0, keep], Y[1, keep]) and torch.equal(Q[0, keep], Q[1, keep])
+    assert bool(Y[1, 0].isnan().all()) and bool((Q[1, 0] & 0x7F == 0x7F).all())
+    # 1 / sqrt(infinity) = 0: the infinity's own product is NaN, the others are zeros
+    at = torch.arange(K, device="cuda") == 7
+    assert torch.equal(Y[1, 2].isnan(), at) and torch.equal(Q[1, 2] & 0x7F == 0x7F, at)
+    assert int(Q[1, 2][~at].bitwise_and(0x7F).count_nonzero()) == 0
+
+
 def test_norm_agrees_with_the_fp8_quantize_of_exact_rows(osc):
     """Rows whose norm is 1 and whose normed values are bf16: both quantizes see the same values."""
     K = 512

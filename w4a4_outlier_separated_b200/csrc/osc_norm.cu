@@ -121,10 +121,11 @@ __device__ __forceinline__ uint8_t* scale_row(const AddNormParams& p, int row) {
   return p.S + (size_t)(row >> 7) * (p.K >> 7) * 512 + (size_t)((row & 31) * 16 + ((row >> 5) & 3) * 4);
 }
 
-// 1 / sqrt(ss / K + eps), within 2^-22 of it (the root's own error); an all-zero row with eps = 0 stays zero.
+// 1 / sqrt(ss / K + eps), within 2^-22 of it (the root's own error); an all-zero row with eps = 0 stays zero, and a NaN
+// in the row makes all of it NaN.
 __device__ __forceinline__ f2 inverse2(const AddNormParams& p, float ss) {
   const float ms = ss * __frcp_rn((float)p.K) + p.eps;
-  const float inv = ms > 0.f ? rsqrtf(ms) : 0.f;
+  const float inv = ms == 0.f ? 0.f : rsqrtf(ms);
   return pack2(inv, inv);
 }
 
