@@ -289,8 +289,10 @@ OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res,
  * osc_quantize and osc_linear; L = NULL with K_L = 0 multiplies by the 4-bit weights alone. Y: M x N
  * bf16, rounded once from fp32 sums; Yf32 (M x N fp32) may be NULL. One launch, no workspace, any
  * order of calls gives the same bits. For any M up to 1048560, but the weights are read again for
- * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights
- * must be below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). A bad table (an entry >= G, more entries than K_L) is recorded in the status word. */
+ * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights must be
+ * below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). An infinity or
+ * NaN in a token reaches that token's outputs alone. A bad table (an entry >= G, more entries than
+ * K_L) is recorded in the status word. K at most 262144. */
 OSC_API int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
                      const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);
 

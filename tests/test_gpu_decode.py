@@ -340,6 +340,48 @@ def test_gemv_small_values_beside_large_ones(osc):
     assert bool((Y == X[0, 64]).all())
 
 
+@pytest.mark.parametrize("M", [1, 2, 4, 8, 9, 16, 19])
+@pytest.mark.parametrize("where", [7, 300, 301])
+def test_gemv_nan_and_infinity_stay_in_their_rows(osc, M, where):
+    """In a channel of the 4-bit weights, in one of the table."""
+    N, K = 144, 768
+    w = _layer(osc, 1, N, K, 32, 1, 0.7, 6)
+    X = _x(M, K, 3)
+    Y, Yf = _run_gemv(osc, w, X)
+    table = w["L"].view(-1).tolist()
+    c = where // 32 * 32 + table[where // 32] if where == 300 and table[where // 32] >= 0 else where
+    for bad in (float("nan"), float("inf")):
+        X2 = X.clone()
+        X2[M // 2, c] = bad
+        Y2, Yf2 = torch.empty_like(Y), torch.empty_like(Yf)
+        osc.osc_gemv(X2, 32, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], N, Y2, Yf2)
+        keep = [i for i in range(M) if i != M // 2]
+        assert torch.equal(Yf2[keep], Yf[keep]) and torch.equal(Y2[keep], Y[keep])
+        ref = X2[M // 2].double() @ w["W64"][0].t()      # infinity times a zero weight: NaN
+        assert bool(torch.where(ref.isnan(), Yf2[M // 2].isnan(), Yf2[M // 2].double() == ref).all())
+
+
+@pytest.mark.parametrize("M", [1, 5, 16])
+def test_gemv_table_without_channels(osc, M):
+    """A table with no entry set has no W_L columns (K_L = 0): the 4-bit weights alone, and an entry
+    set all the same is reported and left out."""
+    w = _layer(osc, 1, 80, 512, 32, 1, 0.0, 8)
+    X = _x(M, 512, 4)
+    Y, Yf = _run_gemv(osc, w, X)
+    table = torch.full((1, 16, 1), -1, dtype=torch.int8, device="cuda")
+    Y2, Yf2 = torch.empty_like(Y), torch.empty_like(Yf)
+    osc.osc_gemv(X, 32, table, 0, w["QW"], w["SW"], None, 80, Y2, Yf2)
+    assert osc.osc_status() == (0, 0) and torch.equal(Yf, Yf2)
+    Yg = torch.empty_like(Y)
+    osc.osc_gemv_grouped(X, 1, torch.zeros(M, dtype=torch.int32, device="cuda"), 1, 32, table, 0, w["QW"], w["SW"],
+                         None, 80, Yg, Yf2)
+    assert osc.osc_status() == (0, 0)
+    _close(Yg, Yf2, X.double(), w["W64"][0])
+    table[0, 5, 0] = 9
+    osc.osc_gemv(X, 32, table, 0, w["QW"], w["SW"], None, 80, Y2, Yf2)
+    assert osc.osc_status()[0] == -6 and torch.equal(Yf, Yf2)
+
+
 def test_gemv_bad_table_is_reported(osc):
     w = _layer(osc, 1, 128, 512, 32, 1, 0.7, 5)
     X, Y = _x(2, 512, 1), torch.empty((2, 128), dtype=torch.bfloat16, device="cuda")

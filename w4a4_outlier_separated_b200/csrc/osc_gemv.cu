@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     fence_barrier_init();
     if (warp == 0) {
       tma_prefetch_desc(&maps.w);
-      if (n_table) tma_prefetch_desc(&maps.wl);
+      if (n_table && p.K_L) tma_prefetch_desc(&maps.wl);   // without columns there is no map
     }
   }
   __syncthreads();
