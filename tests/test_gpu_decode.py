@@ -312,6 +312,21 @@ def test_gemv_longest_k(osc, M, K, G):
     assert osc.osc_status() == (0, 0)
 
 
+@pytest.mark.parametrize("M,N,K,G", [(1, 544, 6144, 32), (3, 1376, 12288, 32), (2, 1440, 12288, 16), (1, 2560, 32768, 64),
+                                     (5, 1536, 16384, 16), (12, 2576, 16384, 32), (16, 1184, 16384, 64), (8, 672, 12288, 32)])
+def test_gemv_splits(osc, M, N, K, G):
+    """Parts of K over clusters of 2 to 8, with one unit and with several to a cluster, with a table
+    (K = 32768: up to 17 more additions, a warp's items)."""
+    w = _layer(osc, 1, N, K, G, 1, 0.02, N + K + M)
+    X = _x(M, K, N)
+    if K <= 16384:
+        _run_gemv(osc, w, X)
+    else:
+        Y, Yf = torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), torch.empty((M, N), device="cuda")
+        osc.osc_gemv(X, G, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], N, Y, Yf)
+        _close(Y, Yf, X.double(), w["W64"][0], 257)
+
+
 def test_gemv_wide_w_l_and_extremes(osc):
     """K_L wider than the table; tokens of very different and of extreme sizes; weights from 1e-30
     to 1e25; an all-zero token."""

@@ -158,9 +158,9 @@ struct GvSmem {
 };
 // A warp's sums: row r of token m at m * 32 + (r ^ (m / 2 % 4) * 8), so that the mma fragments' stores
 // (tokens 2t, rows g) and the reads (4 rows a lane) meet different banks.
-__host__ __device__ constexpr int gv_sums(int NT) { return 8 * NT * GV_ROWS * 4; }
-__host__ __device__ inline GvSmem gv_smem(int V, int NT, int NW, int ST, int mt, int kc, int cols, int n_table,
-                                          int rows, int E) {
+__host__ __device__ constexpr int gv_sums(int NT, bool two) { return (two ? 2 : 8 * NT) * GV_ROWS * 4; }
+__host__ __device__ inline GvSmem gv_smem(int V, int NT, int NW, int ST, bool two, int mt, int kc, int cols,
+                                          int n_table, int rows, int E) {
   GvSmem m;
   m.stage = GV_ROWS * CH / 2;                                      // codes, or W_L columns
   m.warp = ST * m.stage;
@@ -168,7 +168,7 @@ __host__ __device__ inline GvSmem gv_smem(int V, int NT, int NW, int ST, int mt,
   m.x = m.sc + NW * ST * GV_ROWS * CH / V;                         // tokens in f16
   m.zero = m.x + mt * kc * 2;                                      // 64 bytes of zeros
   m.red = m.zero + 64;                                             // two sets of the warps' sums (NT = 1)
-  m.xs = m.red + (NT == 1 ? 2 * NW * gv_sums(NT) : 0);             // the tokens' powers of two, per item
+  m.xs = m.red + (NT == 1 ? 2 * NW * gv_sums(1, two) : 0);             // the tokens' powers of two, per item
   m.b = (m.xs + kc / CH * NT * 32 + 127) / 128 * 128;              // protected channels' values
   m.bcols = ((cols < n_table ? cols : n_table) + 63) / 64 * 64;
   m.ent = m.b + mt * m.bcols * 2;                                  // table entries with their columns
@@ -207,13 +207,13 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   constexpr int COLS = CH / 4;
   constexpr int SBYTES = GV_ROWS * CH / V;                 // scales of an item
   constexpr int XB = CH / 16;                              // bytes of a lane of an item of a token
-  static_assert(NT == 1 || gv_sums(NT) <= GV_ROWS * RB, "a stage takes a warp's sums");
+  static_assert(NT == 1 || gv_sums(NT, TWO) <= GV_ROWS * RB, "a stage takes a warp's sums");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S;
   const int cta = S == 1 ? blockIdx.x : cluster_id(), rank = S == 1 ? 0 : cluster_ctarank();
   const int N = p.N, K = p.K;
   const int n_table = p.L ? (K >> p.g_shift) * p.R : 0;
-  const GvSmem sm = gv_smem(V, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
+  const GvSmem sm = gv_smem(V, NT, NW, ST, TWO, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0);
   const uint32_t sbase = smem_u32(smem);
   const int swarp = warp * sm.warp, sscale = sm.sc + warp * (ST * SBYTES);
   auto ld32 = [&](int off) { return *reinterpret_cast<const uint32_t*>(smem + off); };
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         // ---- join the team's sums (every warp has had an item): in one of two sets (the other may still
         // be being read), or where these do not fit (NT = 2) in the stage just consumed
         int* const at = reinterpret_cast<int*>(smem + sm.at);
-        int to = red + warp * gv_sums(NT);
+        int to = red + warp * gv_sums(NT, TWO);
         if constexpr (NT == 2) {
           __syncwarp();
           to = swarp + stage * sm.stage;
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           if (m < nt_rows) {
 #pragma unroll 4
             for (int w = team * tw + half; w < team * tw + tw; w += HALVES) {
-              const float4 x = *reinterpret_cast<const float4*>(smem + (NT == 1 ? red + w * gv_sums(NT) : at[w]) + o);
+              const float4 x = *reinterpret_cast<const float4*>(smem + (NT == 1 ? red + w * gv_sums(NT, TWO) : at[w]) + o);
               v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
             }
           }
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           load_next(stage);
           next_stage();
         }
-        if (NT == 1) red = 2 * sm.red + NW * gv_sums(NT) - red;
+        if (NT == 1) red = 2 * sm.red + NW * gv_sums(NT, TWO) - red;
         off += items;
       }
     };
@@ -844,7 +844,7 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int E) {
   return e;
 }
 
-constexpr int GV_SMEM_MAX = 232448 - 8192;                 // 227 KB less the static part and a reserve
+constexpr int GV_SMEM_MAX = 232448 - 4096;                 // 227 KB less the static part (3 KB at most)
 
 template <int V, int NT, int NW, int ST, bool GROUPED, bool TWO>
 cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaStream_t s) {
@@ -871,22 +871,73 @@ cudaError_t launch_t(const GemvMaps& maps, const GemvParams& p, int smem, cudaSt
   return cudaLaunchKernelEx(&cfg, gemv_kernel<V, NT, NW, ST, GROUPED, TWO>, maps, p);
 }
 
+// How many clusters of S = 1 .. 8 CTAs that fill an SM each are resident at once, at (*n)[S]. Clusters of three CTAs
+// and more do not tile the GPCs (45 of three on 148 SMs), and a launch of more runs in two waves: one row, K = 12288, S = 3:
+// 44 clusters 6.5 us, 48 clusters 11.9 us.
+cudaError_t resident_clusters(int num_sms, const int** n) {
+  static PerDeviceOnce once;
+  static int count[PerDeviceOnce::kMaxDevices][9];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run([=] {
+    count[dev][1] = num_sms;
+    const auto kernel = gemv_kernel<32, 1, 16, 2, false, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GV_SMEM_MAX);
+    for (int s = 2; s <= 8 && e == cudaSuccess; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = s;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(s, 1, 1);
+      cfg.blockDim = dim3(16 * 32, 1, 1);
+      cfg.dynamicSmemBytes = GV_SMEM_MAX;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int c = 0;
+      e = cudaOccupancyMaxActiveClusters(&c, kernel, &cfg);
+      count[dev][s] = std::max(1, c);
+    }
+    return e;
+  });
+  *n = e == cudaSuccess ? count[dev] : nullptr;
+  return e;
+}
+
+// S parts of K, one per CTA of a cluster, and what a call with NW warps will take with them, in 10 ns and less what all
+// calls take. A CTA's unit costs 0.12 us an item with 16 warps and 0.16 with 8, which in turn start 0.4 us sooner; the
+// join over the cluster costs a unit 1.5 us, the last one 1.0 (one row). Measured, one row: K = 16384, N = 512 in four
+// parts 6.1 us (two 7.9), N = 1536 in two 8.0 (three, in two waves, 13.4), N = 5120 whole 17.0 (two 19.0).
+struct GvSplit {
+  int S;
+  long long cost;
+};
+GvSplit gv_split(int NW, int max_s, int chunks, long long work, const int* clusters) {
+  GvSplit r{1, 0x7FFFFFFFFFFFFFFFll};
+  for (int S = 1; S <= max_s && (S == 1 || chunks / S >= NW); ++S) {
+    const long long n = (work + clusters[S] - 1) / clusters[S];   // a CTA's units
+    const long long cost = (NW == 16 ? 40 : 0) + n * ((chunks + S - 1) / S) * (NW == 16 ? 12 : 16) + (S > 1 ? 150 * n - 50 : 0);
+    if (cost < r.cost) r = GvSplit{S, cost};
+  }
+  return r;
+}
+
 // The split of one call. NT, NW and ST are the kernel's, p.mt the most tokens of a pass. Where `try_only` and
 // the tokens of a pass would not fit one CTA it returns cudaErrorInvalidValue and launches nothing; else it
 // splits K further, then takes fewer tokens a pass (one always fits within the limits of the entry points).
 template <int NT, int NW, int ST, bool GROUPED, bool TWO = false>
-cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
+cudaError_t launch_v(GemvParams p, bool try_only, const int* clusters, cudaStream_t s) {
   const int V = p.G == 16 ? 16 : 32;
   const int chunks = p.K / CH;
   const int n_table = p.L ? p.K / p.G * p.R : 0;
   auto smem_of = [&](int S) {
     p.kc = (chunks + S - 1) / S * CH;
-    return gv_smem(V, NT, NW, ST, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
+    return gv_smem(V, NT, NW, ST, TWO, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
   };
-  // parts of K: to fill the SMs where units are few, and for the tokens to fit
   const int max_s = GROUPED ? 1 : 8;
-  const long long units = std::max<long long>(1, (long long)p.n_units * ((p.M + p.mt - 1) / p.mt));
-  p.S = std::max(1, std::min({max_s, (int)(num_sms / units), chunks / NW}));
+  auto work_of = [&] { return (long long)p.n_units * ((p.M + p.mt - 1) / p.mt); };
+  p.S = gv_split(NW, max_s, chunks, work_of(), clusters).S;
   while (smem_of(p.S) > GV_SMEM_MAX) {
     if (try_only) return cudaErrorInvalidValue;
     if (p.S < max_s && chunks / (p.S + 1) >= NW) ++p.S;
@@ -896,10 +947,9 @@ cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
   const int smem = smem_of(p.S);
   p.nc_base = chunks / p.S;
   p.nc_more = chunks % p.S;
-  const long long work = (long long)p.n_units * ((p.M + p.mt - 1) / p.mt);
-  p.n_cta = std::max(1, num_sms / p.S);
+  const long long work = work_of();
   // grouped: at most one pass per row
-  p.n_cta = (int)std::min<long long>(p.n_cta, GROUPED ? (long long)p.n_units * p.M : work);
+  p.n_cta = (int)std::min<long long>(clusters[p.S], GROUPED ? (long long)p.n_units * p.M : work);
   p.w_each = work / p.n_cta;
   p.w_more = work % p.n_cta;
   GemvMaps maps;
@@ -911,31 +961,40 @@ cudaError_t launch_v(GemvParams p, bool try_only, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// The variant by the rows alone, and by what fits:
-//   1 .. 8 rows and routed rows: one token tile, 16 warps with two stages each. One or two rows have a kernel of their
-//   own, without the code for more (N = 6144: 7.1 against 7.4 us). Where the tokens and tables leave too little room for
-//   that ring: 8 warps (8 rows of K = 4096: 19.5 us, against 31 us for 16 warps on a K split in two).
+// The variant by the rows, by the time that gv_split expects, and by what fits:
+//   1 .. 8 rows: one token tile, 16 warps with two stages each, or 8 with three where a CTA has few items (one row, N = 544:
+//   K = 2048 4.2 against 4.7 us, K = 6144 in three parts 5.1 against 6.4; N = 6144, K = 4096: 7.5 against 7.1) or the tokens
+//   and tables leave too little room for the first ring (5 rows, K = 12288, N = 4096: 14.3 us, against 16.2 us for 16 warps on
+//   K in three parts). One or two rows have kernels of their own, without the code for more and with room for two rows' sums
+//   alone (N = 6144: 7.1 against 7.4 us; two rows of K = 12288, G = 16: 11.1 against 12.9).
+//   Routed rows: 16 warps, or 8 where these do not fit (33 tokens by 8 experts: 41.7 against 44.8 us).
 //   9 rows and more: two token tiles, 16 rows a pass, 8 warps with the registers of 16 (16 rows, N = 24576: 26.1 us,
 //   against 30.2 us in passes of 8 rows and 31.5 us with 16 warps on items of 128 channels).
-// K is split where the units alone would leave SMs idle (one row, K = 12288, N = 1024: 5.4 against 8.0 us).
 cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   GemvParams p = q;
   p.n_units = p.N / 128 * 4 + std::min(4, p.N % 128 / 8);
   p.g_shift = p.G == 16 ? 4 : p.G == 32 ? 5 : 6;
   p.rows32 = p.N % 32 == 0;
+  const int* clusters;
+  const cudaError_t e = resident_clusters(num_sms, &clusters);
+  if (e != cudaSuccess) return e;
   if (p.expert) {
     p.mt = std::min(p.M, 8);
-    const cudaError_t e = launch_v<1, 16, 2, true>(p, true, num_sms, s);
-    return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 2, true>(p, false, num_sms, s);
+    const cudaError_t e = launch_v<1, 16, 2, true>(p, true, clusters, s);
+    return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 2, true>(p, false, clusters, s);
   }
   if (p.M <= 8) {
     p.mt = p.M;
-    const cudaError_t e = p.M <= 2 ? launch_v<1, 16, 2, false, true>(p, true, num_sms, s)
-                                   : launch_v<1, 16, 2, false>(p, true, num_sms, s);
-    return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 3, false>(p, false, num_sms, s);
+    if (gv_split(16, 8, p.K / CH, p.n_units, clusters).cost <= gv_split(8, 8, p.K / CH, p.n_units, clusters).cost) {
+      const cudaError_t e = p.M <= 2 ? launch_v<1, 16, 2, false, true>(p, true, clusters, s)
+                                     : launch_v<1, 16, 2, false>(p, true, clusters, s);
+      if (e != cudaErrorInvalidValue) return e;
+    }
+    return p.M <= 2 ? launch_v<1, 8, 3, false, true>(p, false, clusters, s)
+                    : launch_v<1, 8, 3, false>(p, false, clusters, s);
   }
   p.mt = std::min(p.M, 16);
-  return launch_v<2, 8, 2, false>(p, false, num_sms, s);
+  return launch_v<2, 8, 2, false>(p, false, clusters, s);
 }
 
 }  // namespace osc
