@@ -292,7 +292,7 @@ OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res,
  * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights must be
  * below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). An infinity or
  * NaN in a token reaches that token's outputs alone. A bad table (an entry >= G, more entries than
- * K_L) is recorded in the status word. K at most 262144. */
+ * K_L) is recorded in the status word. K at most 262144, M x N below 2^36. */
 OSC_API int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
                      const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);
 
@@ -337,8 +337,8 @@ OSC_API int osc_linear_grouped(const uint8_t* QX, const uint8_t* SX, const uint1
  * id < 0 marks an unused row: its Y is zeros. An id >= E is recorded in the status word
  * (OSC_ERR_TABLE) and its row is zeros too. X: (rows + fan - 1) / fan x K; L, QW, SW, WL per expert
  * as in osc_quantize_grouped and osc_linear_grouped (L may be NULL when K_L == 0). Y: rows x N bf16;
- * Yf32 (rows x N) may be NULL. rows and E at most 4096 each, K at most 32768, E x N below 2^31: for more
- * rows use osc_linear_grouped. */
+ * Yf32 (rows x N) may be NULL. rows and E at most 4096 each, K at most 32768, E x N below 2^31, rows x N
+ * below 2^36: for more rows use osc_linear_grouped. */
 OSC_API int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, int E, int K, int G,
                              const int8_t* L, int R, int K_L, const uint8_t* QW, const uint8_t* SW,
                              const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);

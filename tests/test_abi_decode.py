@@ -102,6 +102,9 @@ def test_row_limits(lib, p16):
     assert _gemv(lib, p16, K=262144 + 256, L=None, K_L=0) == -1
     assert _grouped(lib, p16, K=32768 + 256, G=64) == -1
     assert _grouped(lib, p16, E=4096, N=2**19) == -1           # E x N past 31 bits
+    small = dict(K=256, L=None, K_L=0)
+    assert _gemv(lib, p16, M=8192, N=2**23, **small) == -1     # M x N past 36 bits
+    assert _grouped(lib, p16, rows=4096, N=2**24, E=1, **small) == -1
 
 
 def _cpu(*shape, dtype=torch.bfloat16):

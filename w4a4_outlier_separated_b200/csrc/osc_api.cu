@@ -296,7 +296,7 @@ int check_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, i
                const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32) {
   if (R < 1 || R > osc::MAX_R) return OSC_ERR_ARG;
   if (!X || !QW || !SW || !Y || M < 0 || N <= 0 || K <= 0 || K_L < 0) return OSC_ERR_ARG;
-  if ((long long)(N + 127LL) * (K / 32) >= (1LL << 31)) return OSC_ERR_ARG;
+  if ((long long)(N + 127LL) * (K / 32) >= (1LL << 31) || (long long)M * N >= osc::GEMV_MAX_Y) return OSC_ERR_ARG;
   if (L == nullptr && K_L != 0) return OSC_ERR_ARG;
   if (K_L > 0 && !WL) return OSC_ERR_ARG;
   if (K_L > 32767 || (L != nullptr && (long long)(K / G) * R > osc::MAX_TAB)) return OSC_ERR_ARG;

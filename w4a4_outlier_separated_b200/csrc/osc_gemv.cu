@@ -7,8 +7,8 @@
 // the scale layout keeps exactly those rows' words together: 128 contiguous bytes per 512-byte
 // atom. Item: a unit's codes and scales of 256 channels, or its W_L of 64 columns (both 128 bytes a
 // row). The work is the units of every pass (an expert's rows, mt at a time; the dense form is one
-// expert), in one line; each CTA, one per SM, takes an equal run of it, whose parts of one pass are its
-// segments. A segment stages its tokens once; teams of warps share its units, a team's warps a
+// expert), in one line, each pass after some empty places that stand for its start; each CTA, one per SM,
+// takes an equal run of the line, whose parts of one pass are its segments. A segment stages its tokens once; teams of warps share its units, a team's warps a
 // unit's items. Each warp copies its items by TMA into its own ring of stages, running ahead over the
 // ends of units, and computes without waiting for another warp; a unit's sums meet in shared memory
 // in a fixed order. Where units are few, or one CTA cannot hold the tokens, a cluster of S CTAs
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   __shared__ int s_scan[2][NW];
   __shared__ int s_cols[2];             // first W_L column of this CTA's K range, one past the last
   __shared__ int s_list[16];            // the segment's rows of Y (grouped)
+  __shared__ int s_row[3][32];          // up to 32 rows: a row's expert, the rows of that, passes up to and with them
   __shared__ int s_seg[3];              // the segment's expert, rows, first row of its pass (grouped)
   __shared__ __align__(16) float s_sum[GV_ROWS * 8 * NT];
   constexpr int THREADS = NW * 32;
@@ -244,80 +245,85 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   int* const ids = reinterpret_cast<int*>(smem + sm.ids);
   int* const cnt = reinterpret_cast<int*>(smem + sm.cnt);
   const bool small = GROUPED && p.M <= 32;
-  unsigned same = 0;                                       // small: the rows of this lane's expert
-  int my_id = -1, my_pass = 0;                             // and where it is the first, passes up to and with its own
-  long long w_each = p.w_each, w_more = p.w_more;
+  unsigned w_each = p.w_each, w_more = p.w_more;
   if constexpr (GROUPED) {
     int passes;
     if (small) {
+      int my_id = -1;
       if (lane < p.M) my_id = p.expert[lane];
       if (my_id >= p.E) {
         if (cta == 0 && warp == 0) record_status(p.status, DEV_BAD_TABLE);
         my_id = -1;
       }
-      same = __match_any_sync(0xffffffffu, max(my_id, -1));
-      my_pass = my_id >= 0 && __ffs(same) - 1 == lane ? (__popc(same) + p.mt - 1) / p.mt : 0;
+      const unsigned same = __match_any_sync(0xffffffffu, max(my_id, -1));
+      int my_pass = my_id >= 0 && __ffs(same) - 1 == lane ? (__popc(same) + p.mt - 1) >> p.mt_shift : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, my_pass, o);
         if (lane >= o) my_pass += x;
       }
       passes = __shfl_sync(0xffffffffu, my_pass, 31);
+      // the same from every warp
+      s_row[0][lane] = my_id;
+      s_row[1][lane] = same;
+      s_row[2][lane] = my_pass;
+      __syncwarp();
     } else {
+      const int first_id = tid < p.M ? p.expert[tid] : -1;
       for (int i = tid; i < p.E; i += THREADS) cnt[i] = 0;
       __syncthreads();
       for (int r = tid; r < p.M; r += THREADS) {
-        const int id = p.expert[r];
+        const int id = r == tid ? first_id : p.expert[r];
         ids[r] = id;
         if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
         else if (id >= p.E && cta == 0) record_status(p.status, DEV_BAD_TABLE);
       }
       __syncthreads();
       int n = 0;
-      for (int i = tid; i < p.E; i += THREADS) n += (cnt[i] + p.mt - 1) / p.mt;
+      for (int i = tid; i < p.E; i += THREADS) n += (cnt[i] + p.mt - 1) >> p.mt_shift;
       n = __reduce_add_sync(0xffffffffu, n);
       if (lane == 0) s_scan[0][warp] = n;
       __syncthreads();
       passes = __reduce_add_sync(0xffffffffu, lane < NW ? s_scan[0][lane] : 0);
     }
     // rows without an expert come out as zeros
-    for (int r = blockIdx.x; r < p.M; r += gridDim.x) {
-      const int id = small ? __shfl_sync(0xffffffffu, my_id, r) : ids[r];
+    for (int r = blockIdx.x + warp * gridDim.x; r < p.M; r += gridDim.x * NW) {
+      const int id = small ? s_row[0][r] : ids[r];
       if (id >= 0 && id < p.E) continue;
-      for (int n = tid; n < N; n += THREADS) {
-        p.Y[(size_t)r * N + n] = 0;
-        if (p.Yf32) p.Yf32[(size_t)r * N + n] = 0.f;
+      for (int n = lane * 4; n < N; n += 128) {
+        *reinterpret_cast<uint2*>(p.Y + (size_t)r * N + n) = make_uint2(0, 0);
+        if (p.Yf32) *reinterpret_cast<float4*>(p.Yf32 + (size_t)r * N + n) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
-    const long long total = (long long)passes * p.n_units;
-    if (total <= 0x7FFFFFFF) {
-      w_each = (unsigned)total / (unsigned)p.n_cta;
-      w_more = (unsigned)total % (unsigned)p.n_cta;
-    } else {
-      w_each = total / p.n_cta;
-      w_more = total % p.n_cta;
-    }
+    const unsigned total = passes ? (unsigned)passes * (p.n_units + p.gap) - p.gap : 0u;
+    w_each = total / (unsigned)p.n_cta;
+    w_more = total - w_each * p.n_cta;
   }
-  // this CTA's run of the work
-  long long wa = cta * w_each + min((long long)cta, w_more);
-  const long long wb = wa + w_each + (cta < w_more ? 1 : 0);
+  // this CTA's run of the line, on which each pass is gap empty places and then its units (the line starts at the
+  // first pass's units)
+  const unsigned pitch = p.n_units + p.gap;
+  unsigned wa = cta * w_each + min((unsigned)cta, w_more) + p.gap;
+  const unsigned wb = wa + w_each + (cta < w_more ? 1 : 0);
 
   int stage = 0;                                           // of the next item to use
   uint32_t parity = 0, xparity = 0;                        // of its barrier, of the tokens'
   bool dead = false;                                       // a wait ran out
   while (wa < wb) {
     // ---- the segment: units u0 .. u1 - 1 of one pass over expert e
-    int e = 0, tile0 = 0, nt_rows, pass = 0;
-    if (wa >= p.n_units) pass = wa <= 0x7FFFFFFF ? (int)((unsigned)wa / (unsigned)p.n_units) : (int)(wa / p.n_units);
-    const int u0 = (int)(wa - (long long)pass * p.n_units);
+    int e = 0, tile0 = 0, nt_rows;
+    const int pass = wa >= pitch ? wa / pitch : 0;
+    const unsigned at0 = pass * pitch + p.gap;             // the place of the pass's first unit
+    const int u0 = max(0, (int)(wa - at0)), u1 = min(p.n_units, (int)(wb - at0));
+    wa = at0 + p.n_units;
+    if (u1 <= u0) break;                                   // the run ends before the pass's units
     if constexpr (!GROUPED) {
       tile0 = pass * p.mt;
       nt_rows = min(p.mt, p.M - tile0);
     } else if (small) {
-      const int l = __ffs(__ballot_sync(0xffffffffu, pass < my_pass)) - 1;
-      const unsigned rows = __shfl_sync(0xffffffffu, same, l);
-      e = __shfl_sync(0xffffffffu, my_id, l);
-      const int n = __popc(rows), before = __shfl_sync(0xffffffffu, my_pass, l) - (n + p.mt - 1) / p.mt;
+      const int l = __ffs(__ballot_sync(0xffffffffu, pass < s_row[2][lane])) - 1;
+      const unsigned rows = s_row[1][l];
+      e = s_row[0][l];
+      const int n = __popc(rows), before = s_row[2][l] - ((n + p.mt - 1) >> p.mt_shift);
       const int first = (pass - before) * p.mt, i = __popc(rows & ((1u << lane) - 1u)) - first;
       nt_rows = min(n - first, p.mt);
       if (rows >> lane & 1 && i >= 0 && i < p.mt) s_list[i] = lane;   // the same from every warp
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       // the expert that has pass number `pass`: 32 experts a warp at a time
       int before = 0;
       for (int b = 0;; b += THREADS) {
-        const int c = b + tid < p.E ? (cnt[b + tid] + p.mt - 1) / p.mt : 0;
+        const int c = b + tid < p.E ? (cnt[b + tid] + p.mt - 1) >> p.mt_shift : 0;
         const int sum = __reduce_add_sync(0xffffffffu, c);
         if (lane == 0) s_scan[1][warp] = sum;
         __syncthreads();
@@ -366,24 +372,15 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       }
       __syncthreads();
     }
-    const int u1 = (int)min((long long)p.n_units, u0 + (wb - wa));
-    wa += u1 - u0;
     // teams of tw warps: the fewest rounds over the teams, a round costing a warp's items and about OV / 4 more for
     // their sums; every warp of a team has items of every unit, and a cluster's CTAs are one team each
     constexpr int LOG_NW = NW == 16 ? 4 : 3, OV = 2;
     static_assert(NW == 1 << LOG_NW, "warps");
     int tw_shift = LOG_NW;
-    if (S == 1) {
-      const int nu = u1 - u0, n = nc + (n_table ? (min(p.K_L, n_table) + COLS - 1) / COLS : 0);
-      int best = 0x7FFFFFFF;
-#pragma unroll
-      for (int i = LOG_NW; i >= 0; --i) {
-        const int cost = ((nu + (NW >> i) - 1) >> (LOG_NW - i)) * (4 * ((n + (1 << i) - 1) >> i) + OV);
-        if (1 << i <= nc && cost < best) {
-          best = cost;
-          tw_shift = i;
-        }
-      }
+    if (S == 1) {                                          // lane i looks at teams of 2^i, the larger of two equal ones wins
+      const int nu = u1 - u0, n = nc + (n_table ? (min(p.K_L, n_table) + COLS - 1) / COLS : 0), i = min(lane, LOG_NW);
+      const int cost = ((nu + (NW >> i) - 1) >> (LOG_NW - i)) * (4 * ((n + (1 << i) - 1) >> i) + OV);
+      tw_shift = 7 - (__reduce_min_sync(0xffffffffu, 1 << i <= nc ? cost * 8 + 7 - i : 0x7FFFFFFF) & 7);
     }
     const int tw = 1 << tw_shift, teams = NW >> tw_shift, team = warp >> tw_shift, twarp = warp & (tw - 1);
     const int8_t* const L = p.L + (size_t)e * n_table;
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     const uint8_t* const sfrom = p.SW + ((size_t)(GROUPED ? e * ((N + 127) / 128) : 0) * satoms +
                                          (size_t)c0 * (CH / V / 4) + (lane >> 3)) * 512 + (lane & 7) * 16;
     auto xrow = [&](int m) -> const uint16_t* {
-      if constexpr (GROUPED) return p.X + (size_t)(s_list[m] / p.fan) * K;
+      if constexpr (GROUPED) return p.X + (size_t)(p.fan_inv ? __umulhi(s_list[m], p.fan_inv) : s_list[m]) * K;
       else return p.X + (size_t)(tile0 + m) * K;
     };
 
@@ -844,6 +841,10 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int E) {
   return e;
 }
 
+// Items that the start of a pass counts for in the cut of the work: a CTA whose run crosses into another pass drains its
+// ring and stages anew, 6000 cycles in which it would multiply some 45 items (16 tokens by 8 experts, K = 768: 19.3 us
+// against 24 us cut by units alone; 33 tokens, K = 2048: 40.1 against 41.7).
+constexpr int GV_GAP = 45;
 constexpr int GV_SMEM_MAX = 232448 - 4096;                 // 227 KB less the static part (3 KB at most)
 
 template <int V, int NT, int NW, int ST, bool GROUPED, bool TWO>
@@ -936,7 +937,8 @@ cudaError_t launch_v(GemvParams p, bool try_only, const int* clusters, cudaStrea
     return gv_smem(V, NT, NW, ST, TWO, p.mt, p.kc, p.K_L, n_table, GROUPED ? p.M : 0, GROUPED ? p.E : 0).total;
   };
   const int max_s = GROUPED ? 1 : 8;
-  auto work_of = [&] { return (long long)p.n_units * ((p.M + p.mt - 1) / p.mt); };
+  p.gap = std::max(1, GV_GAP / chunks);
+  auto work_of = [&] { return (long long)(p.n_units + p.gap) * ((p.M + p.mt - 1) / p.mt) - p.gap; };
   p.S = gv_split(NW, max_s, chunks, work_of(), clusters).S;
   while (smem_of(p.S) > GV_SMEM_MAX) {
     if (try_only) return cudaErrorInvalidValue;
@@ -945,13 +947,15 @@ cudaError_t launch_v(GemvParams p, bool try_only, const int* clusters, cudaStrea
     else return cudaErrorInvalidValue;
   }
   const int smem = smem_of(p.S);
+  while (1 << p.mt_shift < p.mt) ++p.mt_shift;
   p.nc_base = chunks / p.S;
   p.nc_more = chunks % p.S;
   const long long work = work_of();
+  if (work > 0x7FFFFFFF) return cudaErrorInvalidValue;
   // grouped: at most one pass per row
   p.n_cta = (int)std::min<long long>(clusters[p.S], GROUPED ? (long long)p.n_units * p.M : work);
-  p.w_each = work / p.n_cta;
-  p.w_more = work % p.n_cta;
+  p.w_each = (unsigned)(work / p.n_cta);
+  p.w_more = (unsigned)(work % p.n_cta);
   GemvMaps maps;
   const cudaError_t e = encode_gemv_maps(&maps, p, GROUPED ? p.E : 1);
   if (e != cudaSuccess) return e;
@@ -975,11 +979,12 @@ cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   p.n_units = p.N / 128 * 4 + std::min(4, p.N % 128 / 8);
   p.g_shift = p.G == 16 ? 4 : p.G == 32 ? 5 : 6;
   p.rows32 = p.N % 32 == 0;
+  p.fan_inv = (unsigned)(((1LL << 32) + p.fan - 1) / p.fan);   // exact for rows up to GEMV_MAX_ROWS; 0 for a fan of 1
   const int* clusters;
   const cudaError_t e = resident_clusters(num_sms, &clusters);
   if (e != cudaSuccess) return e;
   if (p.expert) {
-    p.mt = std::min(p.M, 8);
+    p.mt = p.M > 4 ? 8 : p.M > 2 ? 4 : p.M;
     const cudaError_t e = launch_v<1, 16, 2, true>(p, true, clusters, s);
     return e != cudaErrorInvalidValue ? e : launch_v<1, 8, 2, true>(p, false, clusters, s);
   }

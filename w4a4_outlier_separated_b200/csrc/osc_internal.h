@@ -104,7 +104,10 @@ struct GemvParams {
   // set by the launcher: parts of K, CTAs per part, 32-row units, most tokens of a pass, channels and 256-channel
   // items of a part, log2 G, whether N is a multiple of 32
   int S, n_cta, n_units, mt, kc, nc_base, nc_more, g_shift, rows32;
-  long long w_each, w_more;   // units of each CTA, CTAs with one more (dense)
+  int mt_shift;               // grouped: log2 mt
+  int gap;                    // units that the start of a pass counts for in the cut of the work
+  unsigned fan_inv;           // grouped: 2^32 / fan, rounded up (0: fan = 1)
+  unsigned w_each, w_more;    // share of each CTA, CTAs with one more (dense)
 };
 struct GemvMaps {
   CUtensorMap w, wl;
@@ -117,6 +120,8 @@ constexpr int GEMV_MAX_ROWS = 4096;
 constexpr int GEMV_MAX_EXPERTS = 4096;
 // longest K: one token of a CTA's part fits in shared memory beside the weight ring (dense: K in up to 8 parts)
 constexpr int GEMV_MAX_K = 262144;
+// M x N stays below this, so that 32 bits count the units of all passes
+constexpr long long GEMV_MAX_Y = 1LL << 36;
 constexpr int GEMV_GROUPED_MAX_K = 32768;
 cudaError_t launch_gemv(const GemvParams& p, int num_sms, cudaStream_t s);
 
