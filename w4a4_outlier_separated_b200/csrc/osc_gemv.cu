@@ -27,7 +27,7 @@
 // with W_L run as bf16 mma into the same sums.
 //
 // Measured (B200, launches back to back in a graph, weights cold): K = 4096, one token, N = 98304 (201 MB):
-// 37.8 us, 5.3 TB/s, 86 % of the copy bandwidth. N = 24576: 13.7 us against a floor of 8.5; N = 6144: 7.0 us
+// 37.0 us, 5.4 TB/s, 88 % of the copy bandwidth. N = 24576: 13.5 us against a floor of 8.5; N = 6144: 6.9 us
 // against 2.2. What is left there is the start, about 5000 cycles before the first item is multiplied
 // (the tokens' and the table's round trip, their conversion by every CTA), and 1.3 or 5.2 units to an SM. In
 // the stream itself the ALU pipe (two cycles a conversion) and the memory are about even: 460 cycles per

@@ -15,10 +15,10 @@
 // row, so that the block maximum meets by shuffles. One CTA per row (or a few short rows): a row's sum
 // needs all of it, so what keeps the memory busy is the other rows' CTAs on the SM.
 //
-// Measured (B200, launches back to back in a graph, inputs cold): 16384 x 4096 with a residual 74.2 us, 6.3 TB/s, 96 % of
-// the copy bandwidth. 2048 x 4096: 12.0 us against 9.0 (the fill and the drain of 14 rows per SM). 4001 x 6144
-// without a residual: 19.8 us against 11.4; there 545 instructions per 1024 channels bind before the memory. One
-// row: 2.0 us, the launch. Measured slower: persistent CTAs with the next row's loads in registers (4001 x 6144: 23.7
+// Measured (B200, launches back to back in a graph, inputs cold): 16384 x 4096 with a residual 73.8 us, 6.4 TB/s, 97 % of
+// the copy bandwidth. 2048 x 4096: 11.7 us against 9.0 (the fill and the drain of 14 rows per SM). 4001 x 6144
+// without a residual: 19.6 us against 11.4; there the instructions bind before the memory (586 of a warp per 1024
+// channels with a residual). One row: 1.9 us, the launch. Measured slower: persistent CTAs with the next row's loads in registers (4001 x 6144: 23.7
 // us) or with a ring of rows in shared memory (31 us): fewer rows are worked on at once.
 #include "osc_device.cuh"
 #include "osc_internal.h"
@@ -232,7 +232,7 @@ static cudaError_t launch_c(const AddNormParams& p, int tpr, cudaStream_t s) {
 
 cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s) {
   // steps per thread: one where rows are few, so that a row has the most threads (one row of 4096: 2.0 against 2.6 us with
-  // four steps), four where they fill the SMs (2048 rows: 12.1 against 13.2 us, 16384 rows: 74 against 90 us)
+  // four steps), four where they fill the SMs (2048 rows: 12 against 13 us, 16384 rows: 74 against 90 us)
   const int nchunk = p.K / 8;
   auto tpr = [&](int c) { return ((nchunk + c - 1) / c + 31) / 32 * 32; };
   int c = p.M >= 4 * num_sms ? 4 : 1;
