@@ -327,6 +327,21 @@ def test_gemv_splits(osc, M, N, K, G):
         _close(Y, Yf, X.double(), w["W64"][0], 257)
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 16, 256), (40, 16, 512), (1000, 16, 256), (333, 80, 768), (100, 4112, 256)])
+def test_gemv_many_passes(osc, M, N, K):
+    """Passes of one to many units, and fewer units than CTAs."""
+    w = _layer(osc, 1, N, K, 32, 1, 0.5, M + N)
+    _run_gemv(osc, w, _x(M, K, M))
+
+
+@pytest.mark.parametrize("E,N,K,rows", [(300, 16, 256, 500), (40, 48, 512, 31), (3, 4112, 256, 100), (1, 32, 256, 2000)])
+def test_grouped_many_passes(osc, E, N, K, rows):
+    w = _layer(osc, E, N, K, 32, 1, 0.5, E)
+    ids = torch.randint(-1, E, (rows,), generator=_gen(rows), device="cuda", dtype=torch.int32)
+    _run_grouped(osc, w, _x(rows, K, E), 1, ids)
+    assert osc.osc_status() == (0, 0)
+
+
 def test_gemv_wide_w_l_and_extremes(osc):
     """K_L wider than the table; tokens of very different and of extreme sizes; weights from 1e-30
     to 1e25; an all-zero token."""

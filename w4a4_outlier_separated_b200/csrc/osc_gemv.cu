@@ -7,12 +7,13 @@
 // the scale layout keeps exactly those rows' words together: 128 contiguous bytes per 512-byte
 // atom. Item: a unit's codes and scales of 256 channels, or its W_L of 64 columns (both 128 bytes a
 // row). The work is the units of every pass (an expert's rows, mt at a time; the dense form is one
-// expert), in one line, each pass after some empty places that stand for its start; each CTA, one per SM,
-// takes an equal run of the line, whose parts of one pass are its segments. A segment stages its tokens once; teams of warps share its units, a team's warps a
-// unit's items. Each warp copies its items by TMA into its own ring of stages, running ahead over the
-// ends of units, and computes without waiting for another warp; a unit's sums meet in shared memory
-// in a fixed order. Where units are few, or one CTA cannot hold the tokens, a cluster of S CTAs
-// splits K and adds its sums through distributed shared memory.
+// expert), in one line, each pass after some empty places that stand for its start; each CTA, one
+// per SM, takes an equal run of the line, whose parts of one pass are its segments. A segment
+// stages its tokens once; teams of warps share its units, a team's warps a unit's items. Each warp
+// copies its items by TMA into its own ring of stages, running ahead over the ends of units, and
+// computes without waiting for another warp; a unit's sums meet in shared memory in a fixed order.
+// Where units are few, or one CTA cannot hold the tokens, a cluster of S CTAs splits K and adds its
+// sums through distributed shared memory.
 //
 // Arithmetic: mma.m16n8k16 on f16 operands with fp32 accumulators, the weight rows as the
 // 16-row side and the tokens as the 8-wide side. E2M1 codes become f16 exactly (one conversion
