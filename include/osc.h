@@ -287,7 +287,9 @@ OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res,
  * with ch_i the channel of table entry i: the table's channels meet their bf16 weights W_L, as in
  * the §3.2 equation, and no other value is quantized. X: M x K bf16. L, R, K_L, WL as
  * osc_quantize and osc_linear; L = NULL with K_L = 0 multiplies by the 4-bit weights alone. Y: M x N
- * bf16, rounded once from fp32 sums; Yf32 (M x N fp32) may be NULL. One launch, no workspace, any
+ * bf16, rounded once from fp32 sums; Yf32 (M x N fp32) may be NULL. A token's values keep all their bits
+ * down to 2^-130 of its largest unprotected value in the same 256 channels (k / 256); below 2^-31 of it the
+ * call takes up to twice as long. One launch, no workspace, any
  * order of calls gives the same bits. For any M up to 1048560, but the weights are read again for
  * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights must be
  * below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). An infinity or

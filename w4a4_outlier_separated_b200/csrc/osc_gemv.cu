@@ -19,9 +19,15 @@
 // 16-row side and the tokens as the 8-wide side. E2M1 codes become f16 exactly (one conversion
 // per two codes). The bf16 tokens become f16 after scaling each token's 256 channels by the power
 // of two that puts their largest magnitude in [2^14, 2^15): a value keeps all its bits down to
-// 2^-31 of that maximum, and below that errs by at most 2^-39 of it, far under the fp32 sum's own
-// rounding. A scale block's products are summed in fp32, then multiplied by the weight's and the
-// token's powers of two (exact) and added in fp32. Y is rounded once.
+// 2^-31 of that maximum. Where a value lies below (against weights that are zero at the large channels the
+// small ones are all there is), the segment's tokens are staged once more, as bf16 and 2^112 times larger, and
+// its weights become bf16 2^-112 times theirs (the f16 exponent in bf16's place): the products are the same
+// numbers, and a value keeps its bits down to 2^-130 of the maximum. Such a call takes 1.5 to 2 times as long (K = 4096,
+// N = 24576, one row: 24.7 against 13.9 us; 16 rows: 38.8 against 22.7), which is why the others stay in f16. Looking
+// for such values costs three minima for each eight values, 0 to 3 % of a call; a zero among them takes a second look
+// (1.3 us at one row, 4.9 us at 16).
+// A scale block's products are summed in fp32, then multiplied by the weight's and the token's powers of two (exact) and
+// added in fp32. Y is rounded once.
 // With one or two tokens an mma takes four scale blocks at once, each in columns of its own (two with up to
 // four tokens): a quarter of the scalings and of the shared-memory reads.
 // The protected channels are zeroed in the staged tokens and kept apart in bf16; their products
@@ -101,6 +107,9 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// An E2M1 value as f16 (a pair of them) to the bf16 that is 2^-112 of it: the exponent of 5 bits in the place of 8.
+__device__ __forceinline__ uint32_t f16_to_bf16_2m112(uint32_t h) { return (h >> 3 & 0x0FFF0FFFu) | (h & 0x80008000u); }
+
 // the same onto zero
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -135,6 +144,26 @@ __device__ __forceinline__ uint32_t maxabs2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// min(|a|, |b|) per bf16 half; the sign bits of the result are junk.
+__device__ __forceinline__ uint32_t minabs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Whether one of eight bf16 values is not zero and has an exponent below am - 31. A magnitude less 1, with the top bit
+// turned, is in the order of signed 16-bit numbers, zero the largest.
+__device__ __forceinline__ bool below(const uint4& q, uint32_t am) {
+  auto key = [](uint32_t w) { return (w & 0x7FFF7FFFu) + 0x7FFF7FFFu; };
+  auto least = [](uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  };
+  const uint32_t m = least(least(key(q.x), key(q.y)), least(key(q.z), key(q.w)));
+  return min((int)(short)m, (int)m >> 16) < (int)(max(am, 31u) - 31u) * 128 - 32769;
 }
 
 // Rows lr .. lr + 3 of unit u (in one octet), row r of Y.
@@ -488,6 +517,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     // different banks)
     mbar_wait(smem_u32(&s_xbar), xparity, &s_abort, p.status);
     xparity ^= 1;
+    bool low = false;                                      // the lane has met a value that f16 has cut, or a zero
     auto convert = [&](auto mb) {
       constexpr int MB = decltype(mb)::value;              // tokens at a time, for their latencies' sake
       for (int c = warp; c < nc; c += NW) {
@@ -495,13 +525,14 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         const int grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
         uint8_t* const xc = smem + sm.x + c * CH * 2;
         for (int m0 = 0; m0 < nt_rows; m0 += MB) {
-          uint32_t v[MB][XB / 4], am[MB];
+          uint32_t v[MB][XB / 4], am[MB], mn[MB];          // mn: least magnitudes, protected ones among them
 #pragma unroll
           for (int y = 0; y < MB; ++y) {
             const int m = MB == 1 ? m0 : min(m0 + y, nt_rows - 1);
             const uint8_t* const x = xc + m * p.kc * 2 + lane * XB;
             const uint4 q = *reinterpret_cast<const uint4*>(x);
             v[y][0] = q.x; v[y][1] = q.y; v[y][2] = q.z; v[y][3] = q.w;
+            mn[y] = minabs2(minabs2(q.x, q.y), minabs2(q.z, q.w));
           }
           if (n_table)
             for (int r = 0; r < p.R; ++r) {
@@ -543,6 +574,11 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
             *reinterpret_cast<uint4*>(x) = make_uint4(v[y][0], v[y][1], v[y][2], v[y][3]);
             if (lane == 0) *reinterpret_cast<float*>(smem + sm.xs + (c * 8 * NT + m) * 4) = __uint_as_float((am[y] - 14u) << 23);
           }
+          // a half keeps its top bit where its magnitude is 2^-31 of the maximum or more
+          uint32_t high = 0x80008000u;
+#pragma unroll
+          for (int y = 0; y < MB; ++y) high &= (mn[y] | 0x80008000u) - (max(am[y], 31u) - 31u) * 0x00800080u;
+          low |= high != 0x80008000u;
         }
       }
     };
@@ -553,15 +589,64 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       load_next(pstage);
       pstage = pstage + 1 == ST ? 0 : pstage + 1;
     }
-    __syncthreads();
+    // rare: a look at the tokens as they came, and where one has a value that f16 has cut, every item anew as bf16
+    bool wide = false;
+    if (__builtin_expect(__syncthreads_or(low), 0)) {
+      wide = true;
+      for (int turn = 0; turn < 2 && wide; ++turn) {
+        constexpr int MB = NT * 4;                         // tokens at a time, for their latencies' sake
+        bool cut = turn > 0;
+        for (int c = warp; c < nc; c += NW) {
+          const int k = (c0 + c) * CH + lane * (CH / 32), grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
+          for (int m0 = 0; m0 < nt_rows; m0 += MB) {
+            uint4 q[MB];
+#pragma unroll
+            for (int y = 0; y < MB; ++y) q[y] = *reinterpret_cast<const uint4*>(xrow(min(m0 + y, nt_rows - 1)) + k);
+            for (int r = 0; n_table && r < p.R; ++r) {
+              const int w = ent[grp + r], at = (w & 255) - local;
+              if (w < 0 || at < 0 || at >= CH / 32) continue;
+              const uint32_t keep = ~(0xFFFFu << (at & 1) * 16);
+#pragma unroll
+              for (int y = 0; y < MB; ++y) {
+                if (at >> 1 == 0) q[y].x &= keep;
+                if (at >> 1 == 1) q[y].y &= keep;
+                if (at >> 1 == 2) q[y].z &= keep;
+                if (at >> 1 == 3) q[y].w &= keep;
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < MB; ++y) {
+              const int m = m0 + y;
+              if (m >= nt_rows) continue;
+              const uint32_t xs = ld32(sm.xs + (c * 8 * NT + m) * 4);
+              if (turn == 0) {
+                const uint32_t am = (xs >> 23) + 14;
+                cut |= am < 255 && below(q[y], am);        // beside infinities and NaN there is no sum to keep
+                continue;
+              }
+              // the power of two before and 2^112: the maximum comes to [2^126, 2^127)
+              const float f = __uint_as_float((254u << 23) - xs);
+              auto two = [&](uint32_t w) {
+                return pack_bf16x2(__uint_as_float(w << 16) * f * 0x1p112f, __uint_as_float(w & 0xFFFF0000u) * f * 0x1p112f);
+              };
+              *reinterpret_cast<uint4*>(smem + sm.x + c * CH * 2 + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6))) =
+                  make_uint4(two(q[y].x), two(q[y].y), two(q[y].z), two(q[y].w));
+            }
+          }
+        }
+        wide = __syncthreads_or(cut);
+      }
+    }
 
     // ---- the units. P: scale blocks of an mma. An mma's 16 k-slots are four of each lane t; a lane's slots
     // lie in one scale block, 4 / P lanes to a block. Column n of a tile is token n / P against block n % P
     // of the step alone: the B operand of lane (g, t) is zero where its block is not g % P, so that the P
     // blocks' sums stay apart and one scale each is enough for a step of P blocks. Rows: lane g takes
     // row rg of each octet, the bit reversal of g, so that neighbours' equal pieces meet different banks.
-    auto run = [&](auto pc) {
+    // WIDE: the tokens are staged as bf16.
+    auto run = [&](auto pc, auto wc) {
       constexpr int P = decltype(pc)::value;
+      constexpr bool WIDE = decltype(wc)::value;
       constexpr int STEP = V * P;                          // channels of a step
       constexpr int LB = STEP / 8;                         // a lane's code bytes of a step and row
       const int rg = (g & 1) << 2 | (g & 2) | g >> 2;
@@ -678,6 +763,11 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
                   if (st % PAIR == 0) {
                     load_codes<LB>(smem + w0b + a * 16 * RB, fl[a]);
                     load_codes<LB>(smem + w0b + (a * 16 + 8) * RB, fh[a]);
+#pragma unroll
+                    for (int i = 0; WIDE && i < LN; ++i) {
+                      fl[a][i] = f16_to_bf16_2m112(fl[a][i]);
+                      fh[a][i] = f16_to_bf16_2m112(fh[a][i]);
+                    }
                   }
                   const uint32_t* const l = fl[a] + st % PAIR * 2, *const h8 = fh[a] + st % PAIR * 2;
                   const float s0 = sc[2 * a][st][0], s1 = sc[2 * a][st][NS - 1];
@@ -685,9 +775,15 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
 #pragma unroll
                   for (int b = 0; b < NT; ++b) {
                     float d[4];
-                    mma_f16_first(d, l[0], h8[0], l[1], h8[1], xb[b][0], xb[b][1]);
+                    if constexpr (WIDE) {
+                      d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
-                    for (int i = 2; i < STEP / 8; i += 2) mma_f16(d, l[i], h8[i], l[i + 1], h8[i + 1], xb[b][i], xb[b][i + 1]);
+                      for (int i = 0; i < STEP / 8; i += 2) mma_bf16(d, l[i], h8[i], l[i + 1], h8[i + 1], xb[b][i], xb[b][i + 1]);
+                    } else {
+                      mma_f16_first(d, l[0], h8[0], l[1], h8[1], xb[b][0], xb[b][1]);
+#pragma unroll
+                      for (int i = 2; i < STEP / 8; i += 2) mma_f16(d, l[i], h8[i], l[i + 1], h8[i + 1], xb[b][i], xb[b][i + 1]);
+                    }
                     cs[a][b][0] = fmaf(d[0], s0, cs[a][b][0]);
                     cs[a][b][1] = fmaf(d[1], s1, cs[a][b][1]);
                     cs[a][b][2] = fmaf(d[2], s2, cs[a][b][2]);
@@ -805,10 +901,12 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
         off += items;
       }
     };
-    if (NT == 2) run(std::integral_constant<int, 1>{});
-    else if (TWO || nt_rows <= 2) run(std::integral_constant<int, 4>{});
-    else if (nt_rows <= 4) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 1>{});
+    const std::false_type plain{};
+    if (__builtin_expect(wide, 0)) run(std::integral_constant<int, TWO ? 4 : 1>{}, std::true_type{});
+    else if (NT == 2) run(std::integral_constant<int, 1>{}, plain);
+    else if (TWO || nt_rows <= 2) run(std::integral_constant<int, 4>{}, plain);
+    else if (nt_rows <= 4) run(std::integral_constant<int, 2>{}, plain);
+    else run(std::integral_constant<int, 1>{}, plain);
     if (wa < wb) {
       fence_proxy_async_smem();                            // the next tokens' copies come after
       __syncthreads();                                     // the list, the table and the tokens are free again
