@@ -304,18 +304,30 @@ def osc_linear_grouped(QX, SX, B, QW, SW, WL, mblock_expert, kl, E: int, Mp: int
                                                           _stream(stream)))
 
 
-# The decoding-step calls below check sizes, strides and devices of every operand: a step makes
-# them one at a time, so the checks are kept to three properties and one address per tensor.
+# The decoding-step calls below check types, sizes, strides and devices of every operand: a step makes
+# them one at a time, so the checks are kept to four properties and one address per tensor.
 
-def _at(name: str, t, nbytes: int, device: int):
-    """Address of a contiguous tensor of nbytes on CUDA device `device` (None: None)."""
+# The types whose bits an operand may hold; bf16 also travels as 16-bit integers.
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_BYTE = (torch.uint8, torch.int8)
+_E2M1 = (torch.uint8, torch.int8, torch.float4_e2m1fn_x2)
+_E4M3 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, torch.int8, torch.float8_e8m0fnu)
+
+
+def _at(name: str, t, types, nbytes: int, device: int):
+    """Address of a contiguous tensor of nbytes of one of `types` on CUDA device `device` (None: None)."""
     if t is None:
         return None
-    if t.nbytes != nbytes or t.get_device() != device or not t.is_contiguous():
-        if t.get_device() != device:
-            raise ValueError(f"{name}: expected a tensor on device {device}, got one on {t.device}")
-        raise ValueError(f"{name}: expected a contiguous tensor of {nbytes} bytes, got {t.nbytes}")
-    return t.data_ptr()
+    if t.dtype in types and t.nbytes == nbytes and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in types:
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in types)}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on device {device}, got one on {t.device}")
+    raise ValueError(f"{name}: expected a contiguous tensor of {nbytes} bytes, got {t.nbytes}")
 
 
 def _launch(name: str, device: int, stream, args):
@@ -345,17 +357,18 @@ def osc_add_rmsnorm_quantize_fp8(X, res, gamma, eps: float, H, Y, QX8, SX, strea
     d = X.get_device()
     n = M * K
     _launch("osc_add_rmsnorm_quantize_fp8", d, stream,
-            (_at("X", X, 2 * n, d), _at("res", res, 2 * n, d), _at("gamma", gamma, 2 * K, d), eps, M, K,
-             _at("H", H, 2 * n, d), _at("Y", Y, 2 * n, d), _at("QX8", QX8, n, d),
-             _at("SX", SX, (M + 127) // 128 * 4 * K, d)))
+            (_at("X", X, _BF16, 2 * n, d), _at("res", res, _BF16, 2 * n, d), _at("gamma", gamma, _BF16, 2 * K, d),
+             eps, M, K,
+             _at("H", H, _BF16, 2 * n, d), _at("Y", Y, _BF16, 2 * n, d), _at("QX8", QX8, _E4M3, n, d),
+             _at("SX", SX, _E8M0, (M + 127) // 128 * 4 * K, d)))
 
 
 def _weight_at(E: int, K: int, G: int, L, K_L: int, QW, SW, WL, N: int, d: int):
     """(address of L, slots per group, K_L, addresses of QW, SW and WL) of E experts' prepared weights."""
     R = 1 if L is None else _slots(L, E * max(1, K // G))
-    return (_at("L", L, E * (K // G) * R, d), R, K_L, _at("QW", QW, E * N * (K // 2), d),
-            _at("SW", SW, E * ((N + 127) // 128) * 128 * (K // (16 if G == 16 else 32)), d),
-            _at("WL", WL, 2 * E * N * K_L, d) if K_L else None)
+    return (_at("L", L, _BYTE, E * (K // G) * R, d), R, K_L, _at("QW", QW, _E2M1, E * N * (K // 2), d),
+            _at("SW", SW, _E8M0, E * ((N + 127) // 128) * 128 * (K // (16 if G == 16 else 32)), d),
+            _at("WL", WL, _BF16, 2 * E * N * K_L, d) if K_L else None)
 
 
 def osc_gemv(X, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
@@ -366,8 +379,8 @@ def osc_gemv(X, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=No
     M, K = X.shape
     d = X.get_device()
     _launch("osc_gemv", d, stream,
-            (_at("X", X, 2 * M * K, d), M, K, G, *_weight_at(1, K, G, L, K_L, QW, SW, WL, N, d), N,
-             _at("Y", Y, 2 * M * N, d), _at("Yf32", Yf32, 4 * M * N, d)))
+            (_at("X", X, _BF16, 2 * M * K, d), M, K, G, *_weight_at(1, K, G, L, K_L, QW, SW, WL, N, d), N,
+             _at("Y", Y, _BF16, 2 * M * N, d), _at("Yf32", Yf32, _F32, 4 * M * N, d)))
 
 
 def osc_gemv_grouped(X, fan: int, expert, E: int, G: int, L, K_L: int, QW, SW, WL, N: int, Y, Yf32=None, stream=None):
@@ -375,16 +388,14 @@ def osc_gemv_grouped(X, fan: int, expert, E: int, G: int, L, K_L: int, QW, SW, W
     tensor of `rows` ids, < 0: a row of zeros)."""
     if G not in (16, 32, 64):
         _check("osc_gemv_grouped", -3)
-    if expert.dtype != torch.int32:
-        raise ValueError("expert: expected an int32 tensor")
     Mx, K = X.shape
     rows, d = expert.numel(), X.get_device()
     if fan < 1 or Mx != (rows + fan - 1) // fan:
         raise ValueError(f"{rows} rows with fan {fan} need {-(-rows // max(1, fan))} rows of X, got {Mx}")
     _launch("osc_gemv_grouped", d, stream,
-            (_at("X", X, 2 * Mx * K, d), rows, fan, _at("expert", expert, 4 * rows, d), E, K, G,
-             *_weight_at(E, K, G, L, K_L, QW, SW, WL, N, d), N, _at("Y", Y, 2 * rows * N, d),
-             _at("Yf32", Yf32, 4 * rows * N, d)))
+            (_at("X", X, _BF16, 2 * Mx * K, d), rows, fan, _at("expert", expert, _I32, 4 * rows, d), E, K, G,
+             *_weight_at(E, K, G, L, K_L, QW, SW, WL, N, d), N, _at("Y", Y, _BF16, 2 * rows * N, d),
+             _at("Yf32", Yf32, _F32, 4 * rows * N, d)))
 
 
 def osc_selftest_timeout(limit_us: int = 10000, stream=None):
