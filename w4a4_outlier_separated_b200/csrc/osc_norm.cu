@@ -225,9 +225,10 @@ static cudaError_t launch_w(AddNormParams p, int tpr, cudaStream_t s) {
 
 template <int C>
 static cudaError_t launch_c(const AddNormParams& p, int tpr, cudaStream_t s) {
-  const bool whole = C * tpr * 8 == p.K;
-  if (p.res) return whole ? launch_w<C, true, true>(p, tpr, s) : launch_w<C, true, false>(p, tpr, s);
-  return whole ? launch_w<C, false, true>(p, tpr, s) : launch_w<C, false, false>(p, tpr, s);
+  if (C == 1 || C * tpr * 8 == p.K)                        // one step of K % 256 = 0 channels is always whole
+    return p.res ? launch_w<C, true, true>(p, tpr, s) : launch_w<C, false, true>(p, tpr, s);
+  if constexpr (C > 1) return p.res ? launch_w<C, true, false>(p, tpr, s) : launch_w<C, false, false>(p, tpr, s);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_add_rmsnorm_fp8(const AddNormParams& p, int num_sms, cudaStream_t s) {
