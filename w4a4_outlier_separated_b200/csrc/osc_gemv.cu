@@ -23,9 +23,9 @@
 // small ones are all there is), the segment's tokens are staged once more, as bf16 and 2^112 times larger, and
 // its weights become bf16 2^-112 times theirs (the f16 exponent in bf16's place): the products are the same
 // numbers, and a value keeps its bits down to 2^-130 of the maximum. Such a call takes 1.5 to 2 times as long (K = 4096,
-// N = 24576, one row: 24.7 against 13.9 us; 16 rows: 38.8 against 22.7), which is why the others stay in f16. Looking
-// for such values costs three minima for each eight values, 0 to 3 % of a call; a zero among them takes a second look
-// (1.3 us at one row, 4.9 us at 16).
+// N = 24576, one row: 25.3 against 13.8 us; 16 rows: 40.2 against 22.2), which is why the others stay in f16. Looking
+// for such values costs three minima for each eight values, 0 to 0.5 us of a call; a zero among them takes a second look
+// (1.9 us at one row, 5.4 us at 16).
 // A scale block's products are summed in fp32, then multiplied by the weight's and the token's powers of two (exact) and
 // added in fp32. Y is rounded once.
 // With one or two tokens an mma takes four scale blocks at once, each in columns of its own (two with up to
@@ -215,17 +215,79 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
   else asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
+// A look at the tokens of a segment as they came (rows of X by `list`, or from tile0 on), and where one has a value that
+// f16 has cut, all of them anew as bf16: the return value. x, xs: the staged tokens and their powers of two; ent: the table's
+// entries or nullptr; the CTA's items c0 .. c0 + nc - 1. A function of its own, and the bf16 units behind the others, so
+// that the calls that never come here do not fetch their instructions (cold caches, 16 rows of K = 4096, N = 24576: 27.6
+// against 34.4 us with both on the way, one token through 8 experts 9.0 against 12.0).
+template <int NT, int NW, bool GROUPED>
+__device__ __noinline__ bool restage_bf16(const GemvParams& p, uint8_t* x, const uint32_t* xs, const int* ent, const int* list,
+                                          int tile0, int nt_rows, int c0, int nc) {
+  constexpr int MB = NT * 4;                               // tokens at a time, for their latencies' sake
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool wide = true;
+  for (int turn = 0; turn < 2 && wide; ++turn) {
+    bool cut = turn > 0;
+    for (int c = warp; c < nc; c += NW) {
+      const int k = (c0 + c) * CH + lane * (CH / 32), grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
+      for (int m0 = 0; m0 < nt_rows; m0 += MB) {
+        uint4 q[MB];
+#pragma unroll
+        for (int y = 0; y < MB; ++y) {
+          const int m = min(m0 + y, nt_rows - 1);
+          const int row = !GROUPED ? tile0 + m : p.fan_inv ? __umulhi(list[m], p.fan_inv) : list[m];
+          q[y] = *reinterpret_cast<const uint4*>(p.X + (size_t)row * p.K + k);
+        }
+        for (int r = 0; ent && r < p.R; ++r) {
+          const int w = ent[grp + r], at = (w & 255) - local;
+          if (w < 0 || at < 0 || at >= CH / 32) continue;
+          const uint32_t keep = ~(0xFFFFu << (at & 1) * 16);
+#pragma unroll
+          for (int y = 0; y < MB; ++y) {
+            if (at >> 1 == 0) q[y].x &= keep;
+            if (at >> 1 == 1) q[y].y &= keep;
+            if (at >> 1 == 2) q[y].z &= keep;
+            if (at >> 1 == 3) q[y].w &= keep;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < MB; ++y) {
+          const int m = m0 + y;
+          if (m >= nt_rows) continue;
+          const uint32_t two_e = xs[c * 8 * NT + m];
+          if (turn == 0) {
+            const uint32_t am = (two_e >> 23) + 14;
+            cut |= am < 255 && below(q[y], am);            // beside infinities and NaN there is no sum to keep
+            continue;
+          }
+          // the power of two before and 2^112: the maximum comes to [2^126, 2^127)
+          const float f = __uint_as_float((254u << 23) - two_e);
+          auto two = [&](uint32_t w) {
+            return pack_bf16x2(__uint_as_float(w << 16) * f * 0x1p112f, __uint_as_float(w & 0xFFFF0000u) * f * 0x1p112f);
+          };
+          *reinterpret_cast<uint4*>(x + c * CH * 2 + m * p.kc * 2 + ((lane * (CH / 16)) ^ ((m & 1) << 6))) =
+              make_uint4(two(q[y].x), two(q[y].y), two(q[y].z), two(q[y].w));
+        }
+      }
+    }
+    wide = __syncthreads_or(cut);
+  }
+  return wide;
+}
+
 }  // namespace
 
 // V: channels of a scale slot; NT: token tiles of 8; NW: warps; ST: stages per warp; TWO: the
 // passes have one or two tokens.
 template <int V, int NT, int NW, int ST, bool GROUPED, bool TWO>
-__global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvParams p) {
+__global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant__ GemvMaps maps,
+                                                           const __grid_constant__ GemvParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ uint64_t s_full[NW][ST];   // a stage's data has arrived
   __shared__ uint64_t s_xbar;           // the tokens have arrived
   __shared__ int s_abort;
+  __shared__ bool s_wide;               // the segment's tokens are staged as bf16
   __shared__ int s_scan[2][NW];
   __shared__ int s_cols[2];             // first W_L column of this CTA's K range, one past the last
   __shared__ int s_list[16];            // the segment's rows of Y (grouped)
@@ -258,6 +320,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
   if (tid < 16) reinterpret_cast<uint32_t*>(smem + sm.zero)[tid] = 0u;
   if (lane == 0) {
     s_abort = 0;
+    s_wide = false;
     for (int i = 0; i < ST; ++i) mbar_init(bars + i * 8, 33);   // the copying lane, and each lane's scales
     if (warp == 0) mbar_init(smem_u32(&s_xbar), NW);
     fence_barrier_init();
@@ -589,54 +652,10 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       load_next(pstage);
       pstage = pstage + 1 == ST ? 0 : pstage + 1;
     }
-    // rare: a look at the tokens as they came, and where one has a value that f16 has cut, every item anew as bf16
-    bool wide = false;
-    if (__builtin_expect(__syncthreads_or(low), 0)) {
-      wide = true;
-      for (int turn = 0; turn < 2 && wide; ++turn) {
-        constexpr int MB = NT * 4;                         // tokens at a time, for their latencies' sake
-        bool cut = turn > 0;
-        for (int c = warp; c < nc; c += NW) {
-          const int k = (c0 + c) * CH + lane * (CH / 32), grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
-          for (int m0 = 0; m0 < nt_rows; m0 += MB) {
-            uint4 q[MB];
-#pragma unroll
-            for (int y = 0; y < MB; ++y) q[y] = *reinterpret_cast<const uint4*>(xrow(min(m0 + y, nt_rows - 1)) + k);
-            for (int r = 0; n_table && r < p.R; ++r) {
-              const int w = ent[grp + r], at = (w & 255) - local;
-              if (w < 0 || at < 0 || at >= CH / 32) continue;
-              const uint32_t keep = ~(0xFFFFu << (at & 1) * 16);
-#pragma unroll
-              for (int y = 0; y < MB; ++y) {
-                if (at >> 1 == 0) q[y].x &= keep;
-                if (at >> 1 == 1) q[y].y &= keep;
-                if (at >> 1 == 2) q[y].z &= keep;
-                if (at >> 1 == 3) q[y].w &= keep;
-              }
-            }
-#pragma unroll
-            for (int y = 0; y < MB; ++y) {
-              const int m = m0 + y;
-              if (m >= nt_rows) continue;
-              const uint32_t xs = ld32(sm.xs + (c * 8 * NT + m) * 4);
-              if (turn == 0) {
-                const uint32_t am = (xs >> 23) + 14;
-                cut |= am < 255 && below(q[y], am);        // beside infinities and NaN there is no sum to keep
-                continue;
-              }
-              // the power of two before and 2^112: the maximum comes to [2^126, 2^127)
-              const float f = __uint_as_float((254u << 23) - xs);
-              auto two = [&](uint32_t w) {
-                return pack_bf16x2(__uint_as_float(w << 16) * f * 0x1p112f, __uint_as_float(w & 0xFFFF0000u) * f * 0x1p112f);
-              };
-              *reinterpret_cast<uint4*>(smem + sm.x + c * CH * 2 + m * p.kc * 2 + ((lane * XB) ^ ((m & 1) << 6))) =
-                  make_uint4(two(q[y].x), two(q[y].y), two(q[y].z), two(q[y].w));
-            }
-          }
-        }
-        wide = __syncthreads_or(cut);
-      }
-    }
+    // rare: a lane has met a value that f16 has cut, or a zero (the answer in shared memory: a register more spills)
+    if (__builtin_expect(__syncthreads_or(low), 0))
+      s_wide = restage_bf16<NT, NW, GROUPED>(p, smem + sm.x, reinterpret_cast<const uint32_t*>(smem + sm.xs), n_table ? ent : nullptr,
+                                           GROUPED ? s_list : nullptr, tile0, nt_rows, c0, nc);
 
     // ---- the units. P: scale blocks of an mma. An mma's 16 k-slots are four of each lane t; a lane's slots
     // lie in one scale block, 4 / P lanes to a block. Column n of a tile is token n / P against block n % P
@@ -902,11 +921,16 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       }
     };
     const std::false_type plain{};
-    if (__builtin_expect(wide, 0)) run(std::integral_constant<int, TWO ? 4 : 1>{}, std::true_type{});
-    else if (NT == 2) run(std::integral_constant<int, 1>{}, plain);
-    else if (TWO || nt_rows <= 2) run(std::integral_constant<int, 4>{}, plain);
-    else if (nt_rows <= 4) run(std::integral_constant<int, 2>{}, plain);
-    else run(std::integral_constant<int, 1>{}, plain);
+    if (__builtin_expect(!s_wide, 1)) {
+      if (NT == 2) run(std::integral_constant<int, 1>{}, plain);
+      else if (TWO || nt_rows <= 2) run(std::integral_constant<int, 4>{}, plain);
+      else if (nt_rows <= 4) run(std::integral_constant<int, 2>{}, plain);
+      else run(std::integral_constant<int, 1>{}, plain);
+    } else {
+      run(std::integral_constant<int, TWO ? 4 : 1>{}, std::true_type{});
+      __syncthreads();
+      s_wide = false;
+    }
     if (wa < wb) {
       fence_proxy_async_smem();                            // the next tokens' copies come after
       __syncthreads();                                     // the list, the table and the tokens are free again
