@@ -25,7 +25,7 @@
 // numbers, and a value keeps its bits down to 2^-130 of the maximum. Such a call takes 1.5 to 2 times as long (K = 4096,
 // N = 24576, one row: 25.3 against 13.8 us; 16 rows: 40.2 against 22.2), which is why the others stay in f16. Looking
 // for such values costs three minima for each eight values, 0 to 0.5 us of a call; a zero among them takes a second look
-// (1.9 us at one row, 5.4 us at 16).
+// by the lanes that have met one (one zero: 0.9 us at one row, 2.2 us at 16).
 // A scale block's products are summed in fp32, then multiplied by the weight's and the token's powers of two (exact) and
 // added in fp32. Y is rounded once.
 // With one or two tokens an mma takes four scale blocks at once, each in columns of its own (two with up to
@@ -217,18 +217,19 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 // A look at the tokens of a segment as they came (rows of X by `list`, or from tile0 on), and where one has a value that
 // f16 has cut, all of them anew as bf16: the return value. x, xs: the staged tokens and their powers of two; ent: the table's
-// entries or nullptr; the CTA's items c0 .. c0 + nc - 1. A function of its own, and the bf16 units behind the others, so
+// entries or nullptr; the CTA's items c0 .. c0 + nc - 1; low: the warp's items at which the lane looks. A function of its own, and the bf16 units behind the others, so
 // that the calls that never come here do not fetch their instructions (cold caches, 16 rows of K = 4096, N = 24576: 27.6
 // against 34.4 us with both on the way, one token through 8 experts 9.0 against 12.0).
 template <int NT, int NW, bool GROUPED>
 __device__ __noinline__ bool restage_bf16(const GemvParams& p, uint8_t* x, const uint32_t* xs, const int* ent, const int* list,
-                                          int tile0, int nt_rows, int c0, int nc) {
+                                          int tile0, int nt_rows, int c0, int nc, unsigned low) {
   constexpr int MB = NT * 4;                               // tokens at a time, for their latencies' sake
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool wide = true;
   for (int turn = 0; turn < 2 && wide; ++turn) {
     bool cut = turn > 0;
     for (int c = warp; c < nc; c += NW) {
+      if (turn == 0 && !(low >> (c / NW & 31) & 1)) continue;
       const int k = (c0 + c) * CH + lane * (CH / 32), grp = (k >> p.g_shift) * p.R, local = k & (p.G - 1);
       for (int m0 = 0; m0 < nt_rows; m0 += MB) {
         uint4 q[MB];
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     // different banks)
     mbar_wait(smem_u32(&s_xbar), xparity, &s_abort, p.status);
     xparity ^= 1;
-    bool low = false;                                      // the lane has met a value that f16 has cut, or a zero
+    unsigned low = 0;                                      // the warp's items with a value of the lane's that f16 has cut, or a zero
     auto convert = [&](auto mb) {
       constexpr int MB = decltype(mb)::value;              // tokens at a time, for their latencies' sake
       for (int c = warp; c < nc; c += NW) {
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
           uint32_t high = 0x80008000u;
 #pragma unroll
           for (int y = 0; y < MB; ++y) high &= (mn[y] | 0x80008000u) - (max(am[y], 31u) - 31u) * 0x00800080u;
-          low |= high != 0x80008000u;
+          if (high != 0x80008000u) low |= 1u << (c / NW & 31);
         }
       }
     };
@@ -653,9 +654,9 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
       pstage = pstage + 1 == ST ? 0 : pstage + 1;
     }
     // rare: a lane has met a value that f16 has cut, or a zero (the answer in shared memory: a register more spills)
-    if (__builtin_expect(__syncthreads_or(low), 0))
+    if (__builtin_expect(__syncthreads_or(low != 0), 0))
       s_wide = restage_bf16<NT, NW, GROUPED>(p, smem + sm.x, reinterpret_cast<const uint32_t*>(smem + sm.xs), n_table ? ent : nullptr,
-                                           GROUPED ? s_list : nullptr, tile0, nt_rows, c0, nc);
+                                           GROUPED ? s_list : nullptr, tile0, nt_rows, c0, nc, low);
 
     // ---- the units. P: scale blocks of an mma. An mma's 16 k-slots are four of each lane t; a lane's slots
     // lie in one scale block, 4 / P lanes to a block. Column n of a tile is token n / P against block n % P
