@@ -21,8 +21,8 @@
  *   - Inputs must be finite (no NaN / Inf).
  *   - Return value: OSC_OK (0) or a negative OSC_ERR_* code; nothing is launched on error.
  *     A call with zero rows (M = 0) does nothing and returns OSC_OK; its pointers may be NULL.
- *     Errors found by a kernel while it runs (a table entry >= G, more entries than K_L,
- *     a bounded wait that ran out) are recorded in a per-device status word that
+ *     Errors found by a kernel while it runs (a table entry >= G, more entries than K_L, an
+ *     expert id >= E, a bounded wait that ran out) are recorded in a per-device status word that
  *     osc_status() reads and clears. The word is shared by every stream and host thread
  *     using the device in this process; it keeps the first error recorded since it was last
  *     cleared. After OSC_ERR_TIMEOUT, every output written since the last clean osc_status
@@ -80,7 +80,7 @@ enum {
   OSC_ERR_G = -3,        /* G not in {16, 32, 64} */
   OSC_ERR_CUDA = -4,     /* a CUDA runtime/driver call failed; see osc_last_cuda_error() */
   OSC_ERR_TIMEOUT = -5,  /* (from osc_status) a kernel's bounded wait ran out */
-  OSC_ERR_TABLE = -6,    /* (from osc_status) a table entry >= G or more entries than K_L */
+  OSC_ERR_TABLE = -6,    /* (from osc_status) a table entry >= G, more entries than K_L, or an expert id >= E */
   OSC_ERR_DEVICE = -7,   /* the current device is not an sm_100 GPU */
   OSC_ERR_SCRATCH = -8   /* (osc_linear_splitk_noalloc) the call needs more than its fixed scratch */
 };
@@ -289,12 +289,14 @@ OSC_API int osc_add_rmsnorm_quantize_fp8(const uint16_t* X, const uint16_t* res,
  * osc_quantize and osc_linear; L = NULL with K_L = 0 multiplies by the 4-bit weights alone. Y: M x N
  * bf16, rounded once from fp32 sums; Yf32 (M x N fp32) may be NULL. A token's values keep all their bits
  * down to 2^-130 of its largest unprotected value in the same 256 channels (k / 256); below 2^-31 of it the
- * call takes up to twice as long. One launch, no workspace, any
- * order of calls gives the same bits. For any M up to 1048560, but the weights are read again for
- * every 16 rows: from a few dozen rows on quantize and use osc_linear. The 4-bit weights must be
- * below 2^100 in magnitude (a token's channels are summed scaled up to about 2^15). An infinity or
- * NaN in a token reaches that token's outputs alone. A bad table (an entry >= G, more entries than
- * K_L) is recorded in the status word. K at most 262144, M x N below 2^36. */
+ * call takes up to twice as long. One launch, no workspace, any order of calls gives the same bits.
+ * For any M up to 1048560, but the weights are read again for every 16 rows, and for every 8 or fewer
+ * where 16 rows of K do not fit an SM (K from 20000 with the largest tables, from 39000 without one).
+ * osc_quantize_linear with a workspace is faster from 9 rows on at K = 4096, N = 6144 or 24576, and from
+ * 5 rows on at K = 12288, N = 4096. The 4-bit weights must be below 2^100 in magnitude (a token's
+ * channels are summed scaled up to about 2^15). An infinity or NaN in a token reaches that token's
+ * outputs alone. A bad table (an entry >= G, more entries than K_L) is recorded in the status word.
+ * K at most 262144, K/G x R at most 4096, M x N below 2^36. */
 OSC_API int osc_gemv(const uint16_t* X, int M, int K, int G, const int8_t* L, int R, int K_L, const uint8_t* QW,
                      const uint8_t* SW, const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);
 
@@ -335,12 +337,14 @@ OSC_API int osc_linear_grouped(const uint8_t* QX, const uint8_t* SX, const uint1
  * top-k for the gate and up projection (X one row per token, expert the tokens' choices in
  * order), 1 for the down projection (X one row per choice). expert: `rows` ids on the DEVICE, in
  * any order and with any repetition, read by the kernel, so a decoding step needs no plan on the
- * host and no sorting; each chosen expert's weight is read once for every 8 of its rows. An
+ * host and no sorting; each chosen expert's weight is read once for every 8 of its rows (4 from K of
+ * 6000 to 9000, 2 from 12000 to 17000 and 1 from 22000 on, by the table, the rows and E). An
  * id < 0 marks an unused row: its Y is zeros. An id >= E is recorded in the status word
  * (OSC_ERR_TABLE) and its row is zeros too. X: (rows + fan - 1) / fan x K; L, QW, SW, WL per expert
  * as in osc_quantize_grouped and osc_linear_grouped (L may be NULL when K_L == 0). Y: rows x N bf16;
- * Yf32 (rows x N) may be NULL. rows and E at most 4096 each, K at most 32768, E x N below 2^31, rows x N
- * below 2^36: for more rows use osc_linear_grouped. */
+ * Yf32 (rows x N) may be NULL. An expert's bad table is recorded when a row has that id. rows and E at
+ * most 4096 each, K at most 32768, K/G x R at most 4096 (one expert's), E x N below 2^31, rows x N below
+ * 2^36: for more rows use osc_linear_grouped. */
 OSC_API int osc_gemv_grouped(const uint16_t* X, int rows, int fan, const int* expert, int E, int K, int G,
                              const int8_t* L, int R, int K_L, const uint8_t* QW, const uint8_t* SW,
                              const uint16_t* WL, int N, uint16_t* Y, float* Yf32, osc_stream_t stream);

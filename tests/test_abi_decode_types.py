@@ -63,3 +63,10 @@ def test_types_that_name_what_the_bytes_are():
                                  (osc.osc_gemv, a, "QW", torch.float8_e4m3fn)):
         with pytest.raises(ValueError, match=f"^{key}: "):
             call(**{**ok, key: ok[key].view(dtype)})
+
+
+def test_the_table_code_names_expert_ids_too():
+    """osc_gemv_grouped records an expert id past the last under the same code as a bad table."""
+    from w4a4_outlier_separated_b200 import osc
+    text = osc.lib().osc_error_string(-6).decode()
+    assert "table entry" in text and "K_L" in text and "expert id" in text

@@ -20,7 +20,7 @@ namespace osc {
 enum : int {
   DEV_OK = 0,
   DEV_TIMEOUT = 1,     // an mbarrier wait ran out of time
-  DEV_BAD_TABLE = 2,   // a table entry was >= G, or more entries than K_L
+  DEV_BAD_TABLE = 2,   // a table entry was >= G, more entries than K_L, or an expert id >= E
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
