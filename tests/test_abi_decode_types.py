@@ -1,5 +1,7 @@
 """Types of the tensors that the binding of the decoding-step calls takes: those whose bits mean what the library reads
 (bf16 or its bits as 16-bit integers, bytes for codes, scales and tables), and no other of the same size."""
+import ctypes
+
 import pytest
 import torch
 
@@ -67,6 +69,8 @@ def test_types_that_name_what_the_bytes_are():
 
 def test_the_table_code_names_expert_ids_too():
     """osc_gemv_grouped records an expert id past the last under the same code as a bad table."""
-    from w4a4_outlier_separated_b200 import osc
-    text = osc.lib().osc_error_string(-6).decode()
+    from w4a4_outlier_separated_b200 import build
+    f = ctypes.CDLL(build.build()).osc_error_string
+    f.argtypes, f.restype = [ctypes.c_int], ctypes.c_char_p
+    text = f(-6).decode()
     assert "table entry" in text and "K_L" in text and "expert id" in text
