@@ -2,7 +2,7 @@
 under a profiler (one kernel, a few launches, a small device footprint), as opposed to
 bench.py, which sweeps every row.
 
-  python -m w4a4_outlier_separated_b200.profile_case CASE [--launches N] [--m M] [--g G]
+  python -m w4a4_outlier_separated_b200.profile_case CASE [--launches N] [--m M] [--k K] [--g G] [--no-res]
 
 CASE:
   qkv           osc_quantize + osc_linear, QKV projection (K=4096, N=6144), M=--m (2048), G=--g (32)
@@ -14,9 +14,11 @@ CASE:
   w2_fp8        osc_quantize_fp8 + osc_linear_fp8_fallback on the down projection
   moe_gateup    osc_quantize_grouped + osc_linear_grouped, 128 experts, 2048 -> 1536
   moe_down      the same for the expert down projection, 768 -> 2048
-  norm_fp8      osc_add_rmsnorm_quantize_fp8, K=4096, M=--m (2048), with a residual
+  norm_fp8      osc_add_rmsnorm_quantize_fp8, K=--k (4096), M=--m (2048), with a residual (--no-res: without)
   gemv          osc_gemv, FFN up weights (K=4096, N=24576), M=--m (1), G=--g
+  gemv_w2       osc_gemv, down projection weights (K=12288, N=4096), M=--m (1), G=--g
   gemv_moe      osc_gemv_grouped, --m tokens (1) through 8 of 128 experts, 2048 -> 1536, random codes
+  gemv_moe_down the same with a row for each choice, 768 -> 2048
 
 Inputs are the seeded synthetic workloads of inputs.py; tables come from osc_build_table on
 the GPU and weights from osc_prepare_weight (or osc_quantize_fp8), so the set-up launches come
@@ -119,14 +121,17 @@ def _moe(which, launches):
         osc.osc_linear_grouped(QX, SX, B, QW, SW, WL, mbed, kld, E, Mp, N, K, G, K_L, Y)
 
 
-def _norm_fp8(M, K, launches):
+def _norm_fp8(M, K, with_res, launches):
     gen = torch.Generator(device="cuda").manual_seed(1)
     X, res = (torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
     gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
     H = torch.empty_like(X)
     QX, SX, _ = osc.alloc_quantize_outputs(M, K, 32, 0, fp8=True)
     for _ in range(launches):
-        osc.osc_add_rmsnorm_quantize_fp8(X, res, gamma, 1e-6, H, None, QX, SX)
+        if with_res:
+            osc.osc_add_rmsnorm_quantize_fp8(X, res, gamma, 1e-6, H, None, QX, SX)
+        else:
+            osc.osc_add_rmsnorm_quantize_fp8(X, None, gamma, 1e-6, None, None, QX, SX)
 
 
 def _gemv(case, G, M, launches):
@@ -139,24 +144,27 @@ def _gemv(case, G, M, launches):
         osc.osc_gemv(X, G, Ld, K_L, QW, SW, WL, N, Y)
 
 
-def _gemv_moe(T, launches, E=128, K=2048, N=1536, top=8):
+def _gemv_moe(T, launches, E=128, K=2048, N=1536, top=8, fan=8):
     gen = torch.Generator(device="cuda").manual_seed(1)
-    X = torch.randn((T, K), generator=gen, device="cuda").to(torch.bfloat16)
+    X = torch.randn((T * top // fan, K), generator=gen, device="cuda").to(torch.bfloat16)
     QW = torch.randint(0, 256, (E, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
     SW = torch.full((E, osc.osc_scale_bytes(N, K, 32)), 120, dtype=torch.uint8, device="cuda")
     ids = torch.rand((T, E), generator=gen, device="cuda").topk(top, 1).indices.reshape(-1).to(torch.int32)
     Y = torch.empty((T * top, N), dtype=torch.bfloat16, device="cuda")
     for _ in range(launches):
-        osc.osc_gemv_grouped(X, top, ids, E, 32, None, 0, QW, SW, None, N, Y)
+        osc.osc_gemv_grouped(X, fan, ids, E, 32, None, 0, QW, SW, None, N, Y)
 
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("case", choices=["qkv", "qkv_rmsnorm", "weight_bound", "weight_bound_split", "ffn", "w2_osc",
-                                     "w2_fp8", "moe_gateup", "moe_down", "norm_fp8", "gemv", "gemv_moe"])
+                                     "w2_fp8", "moe_gateup", "moe_down", "norm_fp8", "gemv", "gemv_w2", "gemv_moe",
+                                     "gemv_moe_down"])
     ap.add_argument("--launches", type=int, default=4, help="rounds of the workload's kernels")
-    ap.add_argument("--m", type=int, default=None, help="token rows (qkv, norm_fp8: 2048, weight_bound: 16, gemv, gemv_moe: 1)")
-    ap.add_argument("--g", type=int, default=32, help="group size (qkv, ffn)")
+    ap.add_argument("--m", type=int, default=None, help="token rows (qkv, norm_fp8: 2048, weight_bound: 16, gemv*: 1)")
+    ap.add_argument("--k", type=int, default=4096, help="channels (norm_fp8)")
+    ap.add_argument("--no-res", action="store_true", help="no residual (norm_fp8)")
+    ap.add_argument("--g", type=int, default=32, help="group size (qkv, ffn, gemv, gemv_w2)")
     a = ap.parse_args(argv)
     osc.lib()
     if a.case == "qkv":
@@ -172,11 +180,15 @@ def main(argv=None):
     elif a.case == "w2_fp8":
         _fp8(I.w2_case(), a.launches)
     elif a.case == "norm_fp8":
-        _norm_fp8(a.m or 2048, 4096, a.launches)
+        _norm_fp8(a.m or 2048, a.k, not a.no_res, a.launches)
     elif a.case == "gemv":
         _gemv(I.ffn_case(a.g), a.g, a.m or 1, a.launches)
+    elif a.case == "gemv_w2":
+        _gemv(I.w2_case(16), a.g, a.m or 1, a.launches)
     elif a.case == "gemv_moe":
         _gemv_moe(a.m or 1, a.launches)
+    elif a.case == "gemv_moe_down":
+        _gemv_moe(a.m or 1, a.launches, K=768, N=2048, fan=1)
     else:
         _moe(a.case[4:], a.launches)
     torch.cuda.synchronize()
