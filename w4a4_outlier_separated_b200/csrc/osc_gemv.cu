@@ -33,16 +33,17 @@
 // The protected channels are zeroed in the staged tokens and kept apart in bf16; their products
 // with W_L run as bf16 mma into the same sums.
 //
-// Measured (B200, launches back to back in a graph, weights cold): K = 4096, one token, N = 98304 (201 MB):
-// 37.0 us, 5.4 TB/s, 88 % of the copy bandwidth. N = 24576: 13.5 us against a floor of 8.5; N = 6144: 6.9 us
-// against 2.2. What is left there is the start, about 5000 cycles before the first item is multiplied
-// (the tokens' and the table's round trip, their conversion by every CTA), and 1.3 or 5.2 units to an SM. In
-// the stream itself the ALU pipe (two cycles a conversion) and the memory are about even: 460 cycles per
-// item and SM sub-partition. With 9 to 16 tokens the conversion of the tokens takes 5 of 26 us (N = 24576)
-// and the mma's as long as the memory. Measured slower: one warp's ring filled with cp.async instead of TMA
-// (FFN 19 against 17 us at the time), one team of 16 warps per unit (20 against 16.4 us), sums handed over
-// through mbarriers without any team barrier (QKV 7.7 against 7.0 us), two CTAs of 8 warps per SM (same time,
-// 4 rows 19.1 against 16.5 us).
+// Measured (B200, launches back to back in a graph on three sets of inputs in turn): K = 4096, one token, N = 98304
+// (codes and scales of 214 MB, no table): 36.4 us, 5.9 TB/s, 90 % of the copy bandwidth (39.7 us on some runs). N = 24576:
+// 13.7 us against a floor of 8.5; N = 6144: 7.1 us against 2.2 (three sets of it stay in L2; with weights that do not, 7.0
+// too). What is left there is the start, about 5000 cycles before the first item is multiplied (the tokens' and the
+// table's round trip, their conversion by every CTA), and 1.3 or 5.2 units to an SM. In the stream itself the ALU pipe (two
+// cycles a conversion) and the memory are about even: 460 cycles per item and SM sub-partition, by clock stamps in a
+// copy of the kernel. With 9 to 16 tokens the conversion of the tokens takes 5 of 26 us (N = 24576), and after it the
+// two warps of a scheduler do not cover the latencies between dependent instructions (issue 46 %, ALU 38 %, DRAM 24 %).
+// Measured slower: one warp's ring filled with cp.async instead of TMA (FFN 19 against 17 us at the time), one team of 16
+// warps per unit (20 against 16.4 us), sums handed over through mbarriers without any team barrier (QKV 7.7 against
+// 7.0 us), two CTAs of 8 warps per SM (same time, 4 rows 19.1 against 16.5 us).
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -217,9 +218,10 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 // A look at the tokens of a segment as they came (rows of X by `list`, or from tile0 on), and where one has a value that
 // f16 has cut, all of them anew as bf16: the return value. x, xs: the staged tokens and their powers of two; ent: the table's
-// entries or nullptr; the CTA's items c0 .. c0 + nc - 1; low: the warp's items at which the lane looks. A function of its own, and the bf16 units behind the others, so
-// that the calls that never come here do not fetch their instructions (cold caches, 16 rows of K = 4096, N = 24576: 27.6
-// against 34.4 us with both on the way, one token through 8 experts 9.0 against 12.0).
+// entries or nullptr; the CTA's items c0 .. c0 + nc - 1; low: the warp's items at which the lane looks. A function of its
+// own, and the bf16 units behind the others, so that the calls that never come here do not fetch their instructions (cold
+// caches, 16 rows of K = 4096, N = 24576: 27.6 against 34.4 us with both on the way, one token through 8 experts 9.0
+// against 12.0).
 template <int NT, int NW, bool GROUPED>
 __device__ __noinline__ bool restage_bf16(const GemvParams& p, uint8_t* x, const uint32_t* xs, const int* ent, const int* list,
                                           int tile0, int nt_rows, int c0, int nc, unsigned low) {
@@ -966,8 +968,9 @@ cudaError_t encode_gemv_maps(GemvMaps* m, const GemvParams& p, int E) {
 }
 
 // Items that the start of a pass counts for in the cut of the work: a CTA whose run crosses into another pass drains its
-// ring and stages anew, 6000 cycles in which it would multiply some 45 items (16 tokens by 8 experts, K = 768: 19.3 us
-// against 24 us cut by units alone; 33 tokens, K = 2048: 40.1 against 41.7).
+// ring and stages anew, 6000 cycles in which it would multiply some 45 items (16 tokens by 8 experts, K = 768: 19.6 us
+// against 22.3 us cut by units alone; 33 tokens, K = 2048: 39.7 against 40.6). One number for all variants: over eleven
+// calls, grouped and in dense passes, G = 16 to 64, it is the best of 1, 20, 45, 90 and 180 or within 7 % of it.
 constexpr int GV_GAP = 45;
 constexpr int GV_SMEM_MAX = 232448 - 4096;                 // 227 KB less the static part (3 KB at most)
 
@@ -1032,8 +1035,11 @@ cudaError_t resident_clusters(int num_sms, const int** n) {
 
 // S parts of K, one per CTA of a cluster, and what a call with NW warps will take with them, in 10 ns and less what all
 // calls take. A CTA's unit costs 0.12 us an item with 16 warps and 0.16 with 8, which in turn start 0.4 us sooner; the
-// join over the cluster costs a unit 1.5 us, the last one 1.0 (one row). Measured, one row: K = 16384, N = 512 in four
-// parts 6.1 us (two 7.9), N = 1536 in two 8.0 (three, in two waves, 13.4), N = 5120 whole 17.0 (two 19.0).
+// join over the cluster costs a unit 1.5 us, the last one 1.0: figures of one row. With more rows, or G = 16, an item and
+// the join both cost more, so the same choice comes out well: forced to every other number of parts, calls of 1 to 16
+// rows, G = 16 to 64, K = 4096 to 16384 were at most 3 % faster, but for 16 rows of K = 12288, N = 1536 (three parts 14.0
+// us, four 12.4). One row, K = 12288, N = 4096: whole 8.3 us, two parts 11.2; 16 rows, N = 2048, K = 4096: two parts 6.8
+// us, whole 8.7; 16 rows, K = 16384, N = 512, G = 16: eight parts 9.4 us, six 9.4, seven (in two waves) 13.2.
 struct GvSplit {
   int S;
   long long cost;
@@ -1091,12 +1097,12 @@ cudaError_t launch_v(GemvParams p, bool try_only, const int* clusters, cudaStrea
 
 // The variant by the rows, by the time that gv_split expects, and by what fits:
 //   1 .. 8 rows: one token tile, 16 warps with two stages each, or 8 with three where a CTA has few items (one row, N = 544:
-//   K = 2048 4.2 against 4.7 us, K = 6144 in three parts 5.1 against 6.4; N = 6144, K = 4096: 7.5 against 7.1) or the tokens
-//   and tables leave too little room for the first ring (5 rows, K = 12288, N = 4096: 14.3 us, against 16.2 us for 16 warps on
-//   K in three parts). One or two rows have kernels of their own, without the code for more and with room for two rows' sums
+//   K = 2048 4.4 against 4.7 us, K = 6144 in three parts 5.1 against 6.4; N = 6144, K = 4096: 7.5 against 7.1) or the tokens
+//   and tables leave too little room for the first ring (5 rows, K = 12288, N = 4096, G = 16: 14.6 us in two parts, against
+//   16.4 us for 16 warps on K in three parts). One or two rows have kernels of their own, without the code for more and with room for two rows' sums
 //   alone (N = 6144: 7.1 against 7.4 us; two rows of K = 12288, G = 16: 11.1 against 12.9).
 //   Routed rows: 16 warps, or 8 where these do not fit (33 tokens by 8 experts: 41.7 against 44.8 us).
-//   9 rows and more: two token tiles, 16 rows a pass, 8 warps with the registers of 16 (16 rows, N = 24576: 26.1 us,
+//   9 rows and more: two token tiles, 16 rows a pass, 8 warps with the registers of 16 (16 rows, N = 24576: 25.9 us,
 //   against 30.2 us in passes of 8 rows and 31.5 us with 16 warps on items of 128 channels).
 cudaError_t launch_gemv(const GemvParams& q, int num_sms, cudaStream_t s) {
   GemvParams p = q;

@@ -17,9 +17,10 @@
 //
 // Measured (B200, launches back to back in a graph, inputs cold): 16384 x 4096 with a residual 73.8 us, 6.4 TB/s, 97 % of
 // the copy bandwidth. 2048 x 4096: 11.7 us against 9.0 (the fill and the drain of 14 rows per SM). 4001 x 6144
-// without a residual: 19.6 us against 11.4; there the instructions bind before the memory (586 of a warp per 1024
-// channels with a residual). One row: 1.9 us, the launch. Measured slower: persistent CTAs with the next row's loads in registers (4001 x 6144: 23.7
-// us) or with a ring of rows in shared memory (31 us): fewer rows are worked on at once.
+// without a residual: 19.6 us against 11.4; neither the issue (63 % of its slots) nor the memory (58 %) is the bound
+// there: 64 registers leave 30 of 64 warps on an SM, whose rows load, reduce and quantize in step and do not hide the
+// loads' latency. One row: 1.9 us, the launch. Measured slower: persistent CTAs with the next row's loads in registers
+// (4001 x 6144: 23.7 us) or with a ring of rows in shared memory (31 us): fewer rows are worked on at once.
 #include "osc_device.cuh"
 #include "osc_internal.h"
 
