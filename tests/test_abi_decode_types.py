@@ -1,7 +1,5 @@
 """Types of the tensors that the binding of the decoding-step calls takes: those whose bits mean what the library reads
 (bf16 or its bits as 16-bit integers, bytes for codes, scales and tables), and no other of the same size."""
-import ctypes
-
 import pytest
 import torch
 
@@ -65,12 +63,3 @@ def test_types_that_name_what_the_bytes_are():
                                  (osc.osc_gemv, a, "QW", torch.float8_e4m3fn)):
         with pytest.raises(ValueError, match=f"^{key}: "):
             call(**{**ok, key: ok[key].view(dtype)})
-
-
-def test_the_table_code_names_expert_ids_too():
-    """osc_gemv_grouped records an expert id past the last under the same code as a bad table."""
-    from w4a4_outlier_separated_b200 import build
-    f = ctypes.CDLL(build.build()).osc_error_string
-    f.argtypes, f.restype = [ctypes.c_int], ctypes.c_char_p
-    text = f(-6).decode()
-    assert "table entry" in text and "K_L" in text and "expert id" in text

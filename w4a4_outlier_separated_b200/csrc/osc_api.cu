@@ -319,7 +319,7 @@ const char* osc_error_string(int code) {
     case OSC_ERR_G: return "group size must be 16, 32 or 64";
     case OSC_ERR_CUDA: return "CUDA call failed (see osc_last_cuda_error)";
     case OSC_ERR_TIMEOUT: return "a kernel wait ran out of time";
-    case OSC_ERR_TABLE: return "table entry out of range, more entries than K_L, or an expert id past the last";
+    case OSC_ERR_TABLE: return "table entry out of range or more entries than K_L";
     case OSC_ERR_DEVICE: return "current device is not an sm_100 GPU";
     case OSC_ERR_SCRATCH: return "the split needs more partials than the fixed 16 MiB scratch holds";
     default: return "unknown error";
