@@ -132,3 +132,57 @@ def test_infinities_beside_spans_of_binades(osc, M):
     keep = [m for m in range(M) if m != 1]
     _close(Y[keep], Yf[keep], X[keep].double(), w["W64"][0])
     assert not bool(torch.isfinite(Yf[1]).any())
+
+
+@pytest.mark.parametrize("G,R,share", [(32, 1, 0.5), (16, 2, 0.4), (64, 1, 0.0)])
+@pytest.mark.parametrize("rows,fan", [(8, 8), (12, 3), (31, 2), (100, 4)])
+def test_grouped_spans_of_binades_shared_rows(osc, G, R, share, rows, fan):
+    """Rows that share an X row, per expert."""
+    E, N, K = 7, 112, 768
+    w = _class_layer(osc, E, N, K, G, R, share, 5)
+    X = _class_tokens((rows + fan - 1) // fan, K, rows)
+    ids = torch.randint(0, E, (rows,), generator=_gen(fan), device="cuda", dtype=torch.int32)
+    Y, Yf = Guarded((rows, N), torch.bfloat16), Guarded((rows, N), torch.float32)
+    osc.osc_gemv_grouped(X, fan, ids, E, G, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], N, Y.t, Yf.t)
+    assert osc.osc_status() == (0, 0)
+    Y.check()
+    Yf.check()
+    for r, e in enumerate(ids.tolist()):
+        _close(Y.t[r:r + 1], Yf.t[r:r + 1], X[r // fan:r // fan + 1].double(), w["W64"][e])
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 7, 16, 20])
+@pytest.mark.parametrize("where", ["one", "some", "padding"])
+def test_zeros_among_the_tokens(osc, M, where):
+    """Zeros are no small values: with zeros in the weights' place instead, the bits are the same."""
+    N, K = 144, 1536
+    g = _gen(M)
+    W = (torch.randn((N, K), generator=g, device="cuda") * 0.02).bfloat16()
+    at = {"one": [777], "some": list(range(5, K, 50)), "padding": list(range(K - 300, K))}[where]
+    X = torch.randn((M, K), generator=g, device="cuda").clamp(-3.9, 3.9).bfloat16()
+    X[X.abs() < 2.0 ** -20] = 1.0
+    X[:, ::256] = 4.0                            # the largest of each run of 256 channels, left alone
+    at = [k for k in at if k % 256]
+    X0 = X.clone()
+    X0[:, at] = 0
+    W[:, at] = 0
+    QW, SW, _ = osc.prepare_weight(W, 32)
+    out = []
+    for x in (X, X0):
+        Y, Yf = torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), torch.empty((M, N), device="cuda")
+        osc.osc_gemv(x, 32, None, 0, QW, SW, None, N, Y, Yf)
+        out.append((Y, Yf))
+    assert torch.equal(out[0][1], out[1][1]) and torch.equal(out[0][0], out[1][0])
+    assert osc.osc_status() == (0, 0)
+
+
+def test_no_rows(osc):
+    """Calls on no rows do nothing, whatever their outputs hold."""
+    w = _class_layer(osc, 1, 32, 256, 32, 1, 0.5, 3)
+    e = lambda *n, d=torch.bfloat16: torch.empty(n, dtype=d, device="cuda")  # noqa: E731
+    osc.osc_gemv(e(0, 256), 32, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], 32, e(0, 32), e(0, 32, d=torch.float32))
+    osc.osc_gemv_grouped(e(0, 256), 4, e(0, d=torch.int32), 1, 32, w["L"], w["K_L"], w["QW"], w["SW"], w["WL"], 32, e(0, 32))
+    osc.osc_add_rmsnorm_quantize_fp8(e(0, 256), e(0, 256), e(256), 1e-6, e(0, 256), e(0, 256), e(0, 256, d=torch.uint8),
+                                     e(0, d=torch.uint8))
+    torch.cuda.synchronize()
+    assert osc.osc_status() == (0, 0)
