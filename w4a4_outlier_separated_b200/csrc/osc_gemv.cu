@@ -103,14 +103,14 @@ __device__ __forceinline__ void load_codes(const uint8_t* from, uint32_t (&h)[LB
   }
 }
 
+// An E2M1 value as f16 (a pair of them) to the bf16 that is 2^-112 of it: the exponent of 5 bits in the place of 8.
+__device__ __forceinline__ uint32_t f16_to_bf16_2m112(uint32_t h) { return (h >> 3 & 0x0FFF0FFFu) | (h & 0x80008000u); }
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// An E2M1 value as f16 (a pair of them) to the bf16 that is 2^-112 of it: the exponent of 5 bits in the place of 8.
-__device__ __forceinline__ uint32_t f16_to_bf16_2m112(uint32_t h) { return (h >> 3 & 0x0FFF0FFFu) | (h & 0x80008000u); }
-
 // the same onto zero
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     // different banks)
     mbar_wait(smem_u32(&s_xbar), xparity, &s_abort, p.status);
     xparity ^= 1;
-    unsigned low = 0;                                      // the warp's items with a value of the lane's that f16 has cut, or a zero
+    unsigned low = 0;                                      // items where the lane has met a value that f16 has cut, or a zero
     auto convert = [&](auto mb) {
       constexpr int MB = decltype(mb)::value;              // tokens at a time, for their latencies' sake
       for (int c = warp; c < nc; c += NW) {
@@ -657,8 +657,8 @@ __global__ void __launch_bounds__(NW * 32, 1) gemv_kernel(const __grid_constant_
     }
     // rare: a lane has met a value that f16 has cut, or a zero (the answer in shared memory: a register more spills)
     if (__builtin_expect(__syncthreads_or(low != 0), 0))
-      s_wide = restage_bf16<NT, NW, GROUPED>(p, smem + sm.x, reinterpret_cast<const uint32_t*>(smem + sm.xs), n_table ? ent : nullptr,
-                                           GROUPED ? s_list : nullptr, tile0, nt_rows, c0, nc, low);
+      s_wide = restage_bf16<NT, NW, GROUPED>(p, smem + sm.x, reinterpret_cast<const uint32_t*>(smem + sm.xs),
+                                             n_table ? ent : nullptr, GROUPED ? s_list : nullptr, tile0, nt_rows, c0, nc, low);
 
     // ---- the units. P: scale blocks of an mma. An mma's 16 k-slots are four of each lane t; a lane's slots
     // lie in one scale block, 4 / P lanes to a block. Column n of a tile is token n / P against block n % P
